@@ -351,7 +351,7 @@ def _own(s):
                     s["workspace"])
         out = {"idx": s["idx"], "w": s["w"]}
         if c["balance"]:
-            out.update(counts=s["counts"], kept=s["kept"], lse=s["lse"], loss=s["loss"][0])
+            out.update(counts=s["counts"], kept=s["kept"], lse=s["lse"], loss=s["loss"])
         return out
     if op == "route_back":
         ep.ep_route_backward(s["logits"], s["mask"], c["mode"], s["idx"], s["w"], s["counts"], s["kept"], s["lse"],
