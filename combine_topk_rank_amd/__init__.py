@@ -24,6 +24,17 @@ The functions keep the C names:
                           workspace, dev_status, stream=None)
     ep_combine(shape, y, topk_idx, topk_w, send_slot, out, dev_status, stream=None)
         (y_rows is y.shape[0])
+    ep_rmsnorm(x, residual, weight, eps, residual_out, y, rows, rstd, stream=None)
+    ep_rmsnorm_backward(r, weight, rstd, grad_y, grad_residual, grad_x, grad_weight,
+                        workspace, stream=None)
+    ep_route(logits, token_mask, mode, topk_idx, topk_w, num_tokens_per_expert, num_tokens,
+             lse, balance_loss, workspace, stream=None)
+    ep_route_backward(logits, token_mask, mode, topk_idx, topk_w, num_tokens_per_expert,
+                      num_tokens, lse, grad_topk_w, grad_balance_loss, grad_logits, stream=None)
+    ep_expert_product(rows, group_offset, w, w_scale, out, dev_status, stream=None)
+    ep_expert_gate_up(rows, group_offset, w, w_scale, out_rows, dev_status, stream=None)
+        (these six take their sizes from the tensors and check every one: a wrong type,
+        shape, device or stride raises ValueError)
     Ring(depth, channels, max_inflight, timeout_ns)   # ep_ring_* calls
 
 Tensors are torch tensors on the current HIP device (contiguous); ``stream``
@@ -54,6 +65,10 @@ EP_FUSED_ONE_KERNEL_LARGE = 102
 EP_FUSED_TWO_CALLS = 103
 EP_FMT_BF16 = 0
 EP_FMT_FP8_E4M3_B128 = 1
+EP_BF16 = 0
+EP_F32 = 1
+EP_GATE_SOFTMAX = 0
+EP_GATE_SOFTMAX_RENORM = 1
 EP_CMD_WRITE = 1
 EP_CMD_ATOMIC = 2
 EP_ATOMIC_ADD = 1
@@ -120,6 +135,23 @@ def _load() -> ctypes.CDLL:
     L.ep_dispatch_ll_fused.restype = ctypes.c_int
     L.ep_combine_ll.argtypes = [S, P, i64, P, P, P, P, P, P]
     L.ep_combine_ll.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    L.ep_rmsnorm.argtypes = [i32, i32, P, P, P, f32, P, P, P, P, P]
+    L.ep_rmsnorm.restype = ctypes.c_int
+    L.ep_rmsnorm_workspace_bytes.argtypes = [i32, i32]
+    L.ep_rmsnorm_workspace_bytes.restype = sz
+    L.ep_rmsnorm_backward.argtypes = [i32, i32, P, P, P, P, P, P, P, P, sz, P]
+    L.ep_rmsnorm_backward.restype = ctypes.c_int
+    L.ep_route_workspace_bytes.argtypes = [i32, i32]
+    L.ep_route_workspace_bytes.restype = sz
+    L.ep_route.argtypes = [i32, i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, sz, P]
+    L.ep_route.restype = ctypes.c_int
+    L.ep_route_backward.argtypes = [i32, i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P]
+    L.ep_route_backward.restype = ctypes.c_int
+    L.ep_expert_product.argtypes = [i32, i64, i32, i32, P, P, P, P, P, P, P]
+    L.ep_expert_product.restype = ctypes.c_int
+    L.ep_expert_gate_up.argtypes = [i32, i64, i32, i32, P, P, P, P, P, P, P]
+    L.ep_expert_gate_up.restype = ctypes.c_int
     L.ep_ring_create.argtypes = [i32, i32, i32, i64]
     L.ep_ring_create.restype = P
     L.ep_ring_destroy.argtypes = [P]
@@ -312,6 +344,204 @@ def ep_combine_ll(s, y, topk_idx, topk_w, expert_slot, out, dev_status, stream=N
     st = lib.ep_combine_ll(ctypes.byref(s), _ptr(y), y.shape[0], _ptr(topk_idx), _ptr(topk_w),
                            _ptr(expert_slot), _ptr(out), _ptr(dev_status), _stream(stream))
     _check(st, "ep_combine_ll")
+
+
+# The calls below take their sizes from the tensors, so they also check each
+# tensor: type, shape, contiguity and the current device.
+
+_U8 = _I32 = _F32 = _BF16 = _E4M3 = None   # torch types, set at the first call
+
+
+def _types() -> None:
+    import torch
+    global _U8, _I32, _F32, _BF16, _E4M3
+    _U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+    _E4M3 = torch.float8_e4m3fn
+
+
+def _arg(name, t, dtype, shape_, device):
+    """Address of tensor t after its checks; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
+    if t.shape != shape_:
+        raise ValueError(f"{name} must have shape {tuple(shape_)}, has {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current device ({device}), is on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _need(name, t):
+    if t is None:
+        raise ValueError(f"{name} must not be None")
+    return t
+
+
+def _call_device(stream):
+    """Current device and the handle of the stream (default: its current one)."""
+    import torch
+    if _U8 is None:
+        _types()
+    device = torch.cuda.current_device()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream must be on the current device ({device}), is on "
+                         f"{stream.device_index}")
+    return device, stream.cuda_stream
+
+
+def _workspace(t, device, needed):
+    if t is None:
+        raise ValueError(f"workspace of {needed} bytes needed")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on the current device ({device})")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def ep_rmsnorm(x, residual, weight, eps, residual_out=None, y=None, rows=None, rstd=None,
+               stream=None) -> None:
+    device, st_ = _call_device(stream)
+    if _need("x", x).dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = sh = x.shape
+    if H < 8 or H % 8 or (rows is not None and H % 128):
+        raise EpError(EP_ERR_INVALID_ARG, "ep_rmsnorm")
+    st = lib.ep_rmsnorm(
+        T, H, _arg("x", x, _BF16, sh, device), _arg("residual", residual, _BF16, sh, device),
+        _arg("weight", _need("weight", weight), _F32, (H,), device), eps,
+        _arg("residual_out", residual_out, _BF16, sh, device), _arg("y", y, _BF16, sh, device),
+        None if rows is None else _arg("rows", rows, _U8,
+                                       (T, ep_row_bytes(H, EP_FMT_FP8_E4M3_B128)), device),
+        _arg("rstd", rstd, _F32, (T,), device), st_)
+    _check(st, "ep_rmsnorm")
+
+
+def ep_rmsnorm_workspace_bytes(T: int, H: int) -> int:
+    return int(lib.ep_rmsnorm_workspace_bytes(T, H))
+
+
+def ep_rmsnorm_backward(r, weight, rstd, grad_y, grad_residual, grad_x, grad_weight, workspace,
+                        stream=None) -> None:
+    device, st_ = _call_device(stream)
+    if _need("r", r).dim() != 2:
+        raise ValueError("r must be [T, H]")
+    T, H = sh = r.shape
+    ws, ws_bytes = (None, 0) if T == 0 else _workspace(workspace, device,
+                                                       ep_rmsnorm_workspace_bytes(T, H))
+    st = lib.ep_rmsnorm_backward(
+        T, H, _arg("r", r, _BF16, sh, device),
+        _arg("weight", _need("weight", weight), _F32, (H,), device),
+        _arg("rstd", _need("rstd", rstd), _F32, (T,), device),
+        _arg("grad_y", _need("grad_y", grad_y), _BF16, sh, device),
+        _arg("grad_residual", grad_residual, _BF16, sh, device),
+        _arg("grad_x", _need("grad_x", grad_x), _BF16, sh, device),
+        _arg("grad_weight", _need("grad_weight", grad_weight), _F32, (H,), device), ws, ws_bytes,
+        st_)
+    _check(st, "ep_rmsnorm_backward")
+
+
+def ep_route_workspace_bytes(T: int, E: int) -> int:
+    return int(lib.ep_route_workspace_bytes(T, E))
+
+
+def _logits_type(logits) -> int:
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if logits.dtype is _F32:
+        return EP_F32
+    if logits.dtype is _BF16:
+        return EP_BF16
+    raise ValueError(f"logits must be float32 or bfloat16, are {logits.dtype}")
+
+
+def ep_route(logits, token_mask, mode, topk_idx, topk_w, num_tokens_per_expert=None,
+             num_tokens=None, lse=None, balance_loss=None, workspace=None, stream=None) -> None:
+    device, st_ = _call_device(stream)
+    kind = _logits_type(_need("logits", logits))
+    if _need("topk_idx", topk_idx).dim() != 2:
+        raise ValueError("topk_idx must be [T, k]")
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    ws, ws_bytes = None, 0
+    if balance_loss is not None or num_tokens is not None or num_tokens_per_expert is not None:
+        ws, ws_bytes = _workspace(workspace, device, ep_route_workspace_bytes(T, E))
+    st = lib.ep_route(
+        T, E, k, kind, mode, _arg("logits", logits, logits.dtype, (T, E), device),
+        _arg("token_mask", token_mask, _U8, (T,), device),
+        _arg("topk_idx", topk_idx, _I32, (T, k), device),
+        _arg("topk_w", _need("topk_w", topk_w), _F32, (T, k), device),
+        _arg("num_tokens_per_expert", num_tokens_per_expert, _I32, (E,), device),
+        _arg("num_tokens", num_tokens, _I32, (1,), device), _arg("lse", lse, _F32, (T,), device),
+        _arg("balance_loss", balance_loss, _F32, (1,), device), ws, ws_bytes, st_)
+    _check(st, "ep_route")
+
+
+def ep_route_backward(logits, token_mask, mode, topk_idx, topk_w, num_tokens_per_expert,
+                      num_tokens, lse, grad_topk_w, grad_balance_loss, grad_logits,
+                      stream=None) -> None:
+    device, st_ = _call_device(stream)
+    kind = _logits_type(_need("logits", logits))
+    if _need("topk_idx", topk_idx).dim() != 2:
+        raise ValueError("topk_idx must be [T, k]")
+    T, E = sh = logits.shape
+    k = topk_idx.shape[1]
+    st = lib.ep_route_backward(
+        T, E, k, kind, mode, _arg("logits", logits, logits.dtype, sh, device),
+        _arg("token_mask", token_mask, _U8, (T,), device),
+        _arg("topk_idx", topk_idx, _I32, (T, k), device),
+        _arg("topk_w", topk_w, _F32, (T, k), device),
+        _arg("num_tokens_per_expert", num_tokens_per_expert, _I32, (E,), device),
+        _arg("num_tokens", num_tokens, _I32, (1,), device),
+        _arg("lse", _need("lse", lse), _F32, (T,), device),
+        _arg("grad_topk_w", grad_topk_w, _F32, (T, k), device),
+        _arg("grad_balance_loss", grad_balance_loss, _F32, (1,), device),
+        _arg("grad_logits", _need("grad_logits", grad_logits), logits.dtype, sh, device), st_)
+    _check(st, "ep_route_backward")
+
+
+def _expert_args(rows, group_offset, w, w_scale, device):
+    """G, M, weight rows, K and the addresses of the four inputs."""
+    if _need("w", w).dim() != 3 or _need("rows", rows).dim() != 2:
+        raise ValueError("w must be [G, N, K] and rows [M, row bytes]")
+    G, N, K = w.shape
+    M = rows.shape[0]
+    if G < 1 or N < 1 or K < 128 or K % 128:
+        raise EpError(EP_ERR_INVALID_ARG, "expert product")
+    if w.dtype is not _U8 and w.dtype is not _E4M3:
+        raise ValueError(f"w must be uint8 or float8_e4m3fn, is {w.dtype}")
+    return (G, M, N, K,
+            _arg("rows", rows, _U8, (M, ep_row_bytes(K, EP_FMT_FP8_E4M3_B128)), device),
+            _arg("group_offset", _need("group_offset", group_offset), _I32, (G + 1,), device),
+            _arg("w", w, w.dtype, (G, N, K), device),
+            _arg("w_scale", _need("w_scale", w_scale), _F32, (G, -(-N // 128), K // 128), device))
+
+
+def ep_expert_product(rows, group_offset, w, w_scale, out, dev_status, stream=None) -> None:
+    device, st_ = _call_device(stream)
+    G, M, N, K, *inputs = _expert_args(rows, group_offset, w, w_scale, device)
+    st = lib.ep_expert_product(G, M, N, K, *inputs,
+                               _arg("out", _need("out", out), _BF16, (M, N), device),
+                               _arg("dev_status", _need("dev_status", dev_status), _I32, (1,),
+                                    device), st_)
+    _check(st, "ep_expert_product")
+
+
+def ep_expert_gate_up(rows, group_offset, w, w_scale, out_rows, dev_status, stream=None) -> None:
+    device, st_ = _call_device(stream)
+    G, M, N, K, *inputs = _expert_args(rows, group_offset, w, w_scale, device)
+    if N % 256:
+        raise EpError(EP_ERR_INVALID_ARG, "ep_expert_gate_up")
+    F = N // 2
+    st = lib.ep_expert_gate_up(G, M, F, K, *inputs,
+                               _arg("out_rows", _need("out_rows", out_rows), _U8,
+                                    (M, ep_row_bytes(F, EP_FMT_FP8_E4M3_B128)), device),
+                               _arg("dev_status", _need("dev_status", dev_status), _I32, (1,),
+                                    device), st_)
+    _check(st, "ep_expert_gate_up")
 
 
 class Ring:
@@ -510,3 +740,52 @@ class BuffersLL(Buffers):
     def combine(self, y, topk_idx, topk_w, stream=None):
         ep_combine_ll(self.shape, y, topk_idx, topk_w, self.expert_slot, self.out,
                       self.dev_status, stream)
+
+
+class BuffersMoE(BuffersLL):
+    """Buffers of a whole mixture-of-experts block over per-expert rows in 8
+    bits (``s.fmt`` EP_FMT_FP8_E4M3_B128): norm, router, dispatch, the experts'
+    two products of inner width ``F`` and combine, in this order."""
+
+    def __init__(self, s: ep_shape_t, F: int, capacity_rows: Optional[int] = None, device="cuda"):
+        import torch
+        if s.fmt != EP_FMT_FP8_E4M3_B128:
+            raise ValueError("the experts take 8-bit rows: fmt must be EP_FMT_FP8_E4M3_B128")
+        super().__init__(s, capacity_rows, device)
+        T, H, k, cap = s.T, s.H, s.k, self.capacity_rows
+        bf, f32 = dict(dtype=torch.bfloat16, device=device), dict(dtype=torch.float32, device=device)
+        self.residual = torch.empty((T, H), **bf)
+        self.normed = torch.empty((T, H), **bf)
+        self.rstd = torch.empty(T, **f32)
+        self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=device)
+        self.topk_w = torch.empty((T, k), **f32)
+        self.inner = torch.empty((cap, ep_row_bytes(F, EP_FMT_FP8_E4M3_B128)), dtype=torch.uint8,
+                                 device=device)
+        self.y = torch.empty((cap, H), **bf)
+
+    def norm(self, x, residual, weight, eps, stream=None):
+        """self.residual = x + residual and self.normed, its norm"""
+        ep_rmsnorm(x, residual, weight, eps, self.residual, self.normed, None, self.rstd, stream)
+
+    def route(self, logits, mode=EP_GATE_SOFTMAX_RENORM, token_mask=None, stream=None):
+        ep_route(logits, token_mask, mode, self.topk_idx, self.topk_w, stream=stream)
+
+    def experts(self, w_gate_up, gate_up_scale, w_down, down_scale, stream=None):
+        """self.y = the experts' outputs for the rows in self.send_buf"""
+        ep_expert_gate_up(self.send_buf, self.expert_offset, w_gate_up, gate_up_scale, self.inner,
+                          self.dev_status, stream)
+        ep_expert_product(self.inner, self.expert_offset, w_down, down_scale, self.y,
+                          self.dev_status, stream)
+
+    def block(self, x, residual, weight, eps, router, w_gate_up, gate_up_scale, w_down, down_scale,
+              mode=EP_GATE_SOFTMAX_RENORM, token_mask=None):
+        """The whole block on the current stream; router(normed) gives the
+        logits [T, E].  Returns the combined output; self.residual is the
+        residual stream that it belongs to."""
+        self.norm(x, residual, weight, eps)
+        self.route(router(self.normed), mode, token_mask)
+        self.layout(self.topk_idx)
+        self.dispatch(self.normed, self.topk_idx, self.topk_w)
+        self.experts(w_gate_up, gate_up_scale, w_down, down_scale)
+        self.combine(self.y, self.topk_idx, self.topk_w)
+        return self.out

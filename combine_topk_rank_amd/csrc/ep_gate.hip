@@ -1,0 +1,522 @@
+// ep_gate.hip — the router: each token's k experts and gate weights from its
+// logits, the experts' counts and the balance loss, and the gradient of the
+// logits.
+//
+//   p[t,:]   = softmax(logits[t,:])
+//   topk_idx = the k largest logits, descending, ties to the lowest expert
+//   topk_w   = p of the chosen, or that divided by its sum over the chosen
+//   f_e = (choices of e) / (n k),  P_e = (sum over kept t of p[t,e]) / n
+//   balance_loss = E * sum_e f_e P_e       (n kept tokens)
+// Backward, with d_e = grad_balance_loss * E * count_e / (n^2 k), z_j =
+// grad_topk_w_j * topk_w_j and S = sum_j z_j:
+//   grad_logits_e = p_e (d_e - sum_i p_i d_i) + sum_{j: e_j = e} z_j
+//                   - (renormalised: sum_{j: e_j = e} topk_w_j S; else p_e S)
+// (the counts are constants of the gradient, as in the loss's definition).
+//
+// A token is a group of L lanes (16 for E <= 256, else a wavefront), each with
+// V consecutive logits in registers; one pass over the logits.  The choices
+// are k rounds of a maximum over the group; float maxima are exact, and the
+// lowest lane that holds the maximum, then its lowest register, is the lowest
+// expert that does.
+
+#include "ep_rows8.h"
+
+namespace ep {
+
+constexpr int kGateBlocks = 256;    // workgroups, and partial sums, of a call with counts
+constexpr int kGateCols = 64;       // experts that a workgroup of the second kernel sums
+
+struct GateArgs {
+    const void* logits;
+    const uint8_t* mask;
+    int32_t* topk_idx;
+    float* topk_w;
+    float* lse;
+    float* part_p;        // [blocks, E]
+    int32_t* part_n;      // [blocks, E]
+    int32_t* part_kept;   // [blocks]
+    int32_t T, E, k, renorm;
+};
+
+template <typename F>
+__device__ inline float load_logit(const void* p, int64_t i);
+template <>
+__device__ inline float load_logit<float>(const void* p, int64_t i) {
+    return reinterpret_cast<const float*>(p)[i];
+}
+template <>
+__device__ inline float load_logit<uint16_t>(const void* p, int64_t i) {
+    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
+}
+
+// The V logits of a lane from expert e0 on; -inf behind the last expert.
+template <typename F, int V>
+__device__ inline void load_logits(const void* p, int64_t base, int e0, int E, float* v) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        v[i] = e0 + i < E ? load_logit<F>(p, base + e0 + i) : -__builtin_inff();
+}
+
+template <typename F, int L, int V, bool STATS>
+__global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
+    extern __shared__ int32_t s_gate[];   // STATS: [E] counts, then [E] float sums
+    constexpr int kGroups = 256 / L;
+    const int sub = (int)threadIdx.x % L, e0 = sub * V;
+    const int group0 = lane_id() & ~(L - 1);            // first lane of this group
+    const uint64_t lanes = L == 64 ? ~0ull : ((1ull << (L & 63)) - 1);
+    float sum_p[V];
+    int kept = 0;
+    if constexpr (STATS) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum_p[i] = 0.0f;
+        for (int e = (int)threadIdx.x; e < a.E; e += 256) s_gate[e] = 0;
+        __syncthreads();
+    }
+    for (int64_t t = (int64_t)blockIdx.x * kGroups + (int)threadIdx.x / L; t < a.T;
+         t += (int64_t)gridDim.x * kGroups) {
+        if (a.mask && !a.mask[t]) {
+            for (int j = sub; j < a.k; j += L) {
+                a.topk_idx[t * a.k + j] = -1;
+                a.topk_w[t * a.k + j] = 0.0f;
+            }
+            if (a.lse && sub == 0) a.lse[t] = 0.0f;
+            continue;
+        }
+        float v[V], x[V];
+        load_logits<F, V>(a.logits, t * a.E, e0, a.E, v);
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, v[i]);
+        top = group_max<L>(top);
+        // a row without a finite logit: every exponential is zero, not NaN
+        const float shift = top == -__builtin_inff() ? 0.0f : top;
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = expf(v[i] - shift);
+            total += x[i];
+        }
+        total = group_sum<L>(total);
+        if constexpr (STATS) {
+            const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum_p[i] += x[i] * inv;
+            kept += sub == 0;
+        }
+        if (a.lse && sub == 0) a.lse[t] = top + logf(total);
+
+        float chosen = 0.0f;                       // exponentials of the chosen
+        float my_w[L == 16 ? 2 : 1];               // lane j holds choices j and j + L
+        int my_e[L == 16 ? 2 : 1];
+#pragma unroll
+        for (int q = 0; q < (L == 16 ? 2 : 1); ++q) {
+            my_w[q] = 0.0f;
+            my_e[q] = -1;
+        }
+        for (int j = 0; j < a.k; ++j) {
+            float m = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < V; ++i) m = fmaxf(m, v[i]);
+            const float best = group_max<L>(m);
+            if (!(best > -__builtin_inff())) break;   // only -inf and NaN are left
+            const uint64_t who = (__ballot(m == best) >> group0) & lanes;
+            const int winner = __builtin_ctzll(who);
+            int at = V;
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i) at = v[i] == best ? i : at;
+            const int e = __shfl(e0 + at, group0 + winner);
+            if (sub == winner) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = i == at ? -__builtin_inff() : v[i];
+            }
+            const float ex = expf(best - shift);
+            chosen += ex;
+#pragma unroll
+            for (int q = 0; q < (L == 16 ? 2 : 1); ++q)
+                if (j == sub + q * L) {
+                    my_w[q] = ex;
+                    my_e[q] = e;
+                }
+            if constexpr (STATS)
+                if (sub == 0) atomicAdd(&s_gate[e], 1);
+        }
+        float scale = 1.0f / (a.renorm ? chosen : total);
+        if (total != total) scale = total;   // a NaN logit makes every weight NaN
+#pragma unroll
+        for (int q = 0; q < (L == 16 ? 2 : 1); ++q) {
+            const int j = sub + q * L;
+            if (j < a.k) {
+                a.topk_idx[t * a.k + j] = my_e[q];
+                a.topk_w[t * a.k + j] = my_e[q] < 0 ? 0.0f : my_w[q] * scale;
+            }
+        }
+    }
+    if constexpr (STATS) {
+        // the groups of a wavefront, then the wavefronts, in a fixed order
+        float* s_sum = reinterpret_cast<float*>(s_gate + a.E);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int o = L; o < 64; o *= 2) sum_p[i] += __shfl_xor(sum_p[i], o);
+        }
+        for (int w = 0; w < 4; ++w) {
+            if ((int)threadIdx.x / kWave == w && lane_id() < L) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (e0 + i < a.E) s_sum[e0 + i] = (w ? s_sum[e0 + i] : 0.0f) + sum_p[i];
+            }
+            __syncthreads();
+        }
+        for (int e = (int)threadIdx.x; e < a.E; e += 256) {
+            a.part_p[(int64_t)blockIdx.x * a.E + e] = s_sum[e];
+            a.part_n[(int64_t)blockIdx.x * a.E + e] = s_gate[e];
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) s_gate[0] = 0;
+        __syncthreads();
+        if (kept) atomicAdd(&s_gate[0], kept);
+        __syncthreads();
+        if (threadIdx.x == 0) a.part_kept[blockIdx.x] = s_gate[0];
+    }
+}
+
+struct GateSumArgs {
+    const float* part_p;
+    const int32_t* part_n;
+    const int32_t* part_kept;
+    int32_t* num_tokens_per_expert;
+    int32_t* num_tokens;
+    float* balance_loss;
+    double* part_loss;      // [workgroups]
+    uint32_t* arrive;       // zero between calls
+    int32_t blocks, E, k;
+};
+
+// Sums the first kernel's partials over its workgroups, kGateCols experts a
+// workgroup; the last workgroup to arrive adds the experts' shares of the loss
+// in their order.
+__global__ __launch_bounds__(256) void gate_sum_kernel(GateSumArgs a) {
+    __shared__ double s_p[4][kGateCols];
+    __shared__ int32_t s_n[4][kGateCols];
+    __shared__ int s_last;
+    const int c = lane_id(), g = (int)threadIdx.x / kWave;
+    const int e = (int)blockIdx.x * kGateCols + c;
+    double p = 0.0;
+    int32_t n = 0;
+    if (e < a.E)
+        for (int b = g; b < a.blocks; b += 4) {
+            p += (double)a.part_p[(int64_t)b * a.E + e];
+            n += a.part_n[(int64_t)b * a.E + e];
+        }
+    s_p[g][c] = p;
+    s_n[g][c] = n;
+    __syncthreads();
+    if (g == 0) {
+        p = ((s_p[0][c] + s_p[1][c]) + s_p[2][c]) + s_p[3][c];
+        n = s_n[0][c] + s_n[1][c] + s_n[2][c] + s_n[3][c];
+        if (e < a.E) a.num_tokens_per_expert[e] = n;
+        double share = e < a.E ? p * (double)n : 0.0;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) share += __shfl_xor(share, o);
+        int last = 0;
+        if (c == 0) {
+            __hip_atomic_store(&a.part_loss[blockIdx.x], share, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+            last = __hip_atomic_fetch_add(a.arrive, 1u, __ATOMIC_ACQ_REL,
+                                          __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+            s_last = last;
+        }
+    }
+    __syncthreads();
+    if (!s_last || g != 0) return;
+    int32_t kept = 0;
+    for (int b = c; b < a.blocks; b += 64) kept += a.part_kept[b];
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) kept += __shfl_xor(kept, o);
+    double loss = 0.0;
+    for (int b = 0; b < (int)gridDim.x; ++b)
+        loss += __hip_atomic_load(&a.part_loss[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (c == 0) {
+        const double m = kept > 0 ? (double)kept : 1.0;
+        a.balance_loss[0] = (float)((double)a.E * loss / (m * m * (double)a.k));
+        a.num_tokens[0] = kept;
+        __hip_atomic_store(a.arrive, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+
+struct GateBackArgs {
+    const void* logits;
+    const uint8_t* mask;
+    const int32_t* topk_idx;
+    const float* topk_w;
+    const float* lse;
+    const int32_t* num_tokens_per_expert;
+    const int32_t* num_tokens;
+    const float* grad_topk_w;
+    const float* grad_balance_loss;
+    void* grad_logits;
+    int32_t T, E, k, renorm;
+};
+
+template <typename F>
+__device__ inline void store_logit(void* p, int64_t i, float v);
+template <>
+__device__ inline void store_logit<float>(void* p, int64_t i, float v) {
+    reinterpret_cast<float*>(p)[i] = v;
+}
+template <>
+__device__ inline void store_logit<uint16_t>(void* p, int64_t i, float v) {
+    reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)bf16_pack(v, 0.0f);
+}
+
+template <typename F, int L, int V>
+__global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
+    constexpr int kGroups = 256 / L;
+    const int sub = (int)threadIdx.x % L, e0 = sub * V;
+    const int group0 = lane_id() & ~(L - 1);
+    float d[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = 0.0f;
+    if (a.grad_balance_loss) {
+        const float n = fmaxf((float)a.num_tokens[0], 1.0f);
+        const float c = a.grad_balance_loss[0] * (float)a.E / n / (n * (float)a.k);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e0 + i < a.E) d[i] = c * (float)a.num_tokens_per_expert[e0 + i];
+    }
+    for (int64_t t = (int64_t)blockIdx.x * kGroups + (int)threadIdx.x / L; t < a.T;
+         t += (int64_t)gridDim.x * kGroups) {
+        float p[V];
+        if (a.mask && !a.mask[t]) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (e0 + i < a.E) store_logit<F>(a.grad_logits, t * a.E + e0 + i, 0.0f);
+            continue;
+        }
+        load_logits<F, V>(a.logits, t * a.E, e0, a.E, p);
+        const float lse = a.lse[t];
+        const float shift = lse == -__builtin_inff() ? 0.0f : lse;
+        float pd = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = expf(p[i] - shift);
+            pd = fmaf(p[i], d[i], pd);
+        }
+        pd = group_sum<L>(pd);
+        float z[L == 16 ? 2 : 1], w[L == 16 ? 2 : 1];   // of choices sub and sub + L
+        int e[L == 16 ? 2 : 1];
+        float S = 0.0f;
+#pragma unroll
+        for (int q = 0; q < (L == 16 ? 2 : 1); ++q) {
+            const int j = sub + q * L;
+            z[q] = w[q] = 0.0f;
+            e[q] = -1;
+            if (j < a.k && a.grad_topk_w) {
+                e[q] = a.topk_idx[t * a.k + j];
+                w[q] = e[q] < 0 ? 0.0f : a.topk_w[t * a.k + j];
+                z[q] = e[q] < 0 ? 0.0f : a.grad_topk_w[t * a.k + j] * w[q];
+            }
+            S += z[q];
+        }
+        S = group_sum<L>(S);
+        if (a.renorm)
+#pragma unroll
+            for (int q = 0; q < (L == 16 ? 2 : 1); ++q) z[q] = fmaf(-w[q], S, z[q]);
+        else
+            pd += S;
+        // p (d - pd), then each choice's part at its expert
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] *= d[i] - pd;
+        for (int j = 0; j < a.k; ++j) {
+            const bool high = j >= L;
+            const int ej = __shfl(high ? e[L == 16 ? 1 : 0] : e[0], group0 + j % L) - e0;
+            const float zj = __shfl(high ? z[L == 16 ? 1 : 0] : z[0], group0 + j % L);
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] += i == ej ? zj : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e0 + i < a.E) store_logit<F>(a.grad_logits, t * a.E + e0 + i, p[i]);
+    }
+}
+
+int check_gate(int32_t T, int32_t E, int32_t k) {
+    if (T < 0 || E < 1 || E > kMaxE || k < 1 || k > kMaxK || k > E) return EP_ERR_INVALID_ARG;
+    if ((int64_t)T * k >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+inline int gate_groups(int E) { return E <= 256 ? 16 : 4; }   // tokens of a workgroup at once
+
+inline int64_t gate_blocks(int32_t T, int32_t E) {
+    const int64_t b = ceil_div(T, gate_groups(E));
+    return b < 1 ? 1 : b > kGateBlocks ? kGateBlocks : b;
+}
+
+inline int64_t sum_blocks(int32_t E) { return ceil_div(E, kGateCols); }
+
+// Workspace: the arrival counter (zero between calls) in a 256-byte line, the
+// experts' shares of the loss, then the first kernel's partials.
+inline size_t gate_workspace(int32_t T, int32_t E) {
+    const size_t b = (size_t)gate_blocks(T, E);
+    return 256 + (size_t)sum_blocks(E) * 8 + b * E * 8 + b * 4;
+}
+
+}  // namespace ep
+
+using namespace ep;
+
+namespace {
+// f(kernel of <float or bf16 bits, lanes, logits a lane>) for E experts.
+#define EP_GATE_SIZES(CALL)                                      \
+    if (E <= 16) return CALL(16, 1);                             \
+    if (E <= 32) return CALL(16, 2);                             \
+    if (E <= 64) return CALL(16, 4);                             \
+    if (E <= 128) return CALL(16, 8);                            \
+    if (E <= 256) return CALL(16, 16);                           \
+    if (E <= 512) return CALL(64, 8);                            \
+    if (E <= 1024) return CALL(64, 16);                          \
+    if (E <= 2048) return CALL(64, 32);                          \
+    return CALL(64, 64)
+
+template <typename F, int L, int V>
+int launch_gate_lv(const GateArgs& a, bool stats, hipStream_t stream) {
+    const int64_t all = ceil_div(a.T, 256 / L);
+    clear_hip_error();
+    if (stats)
+        hipLaunchKernelGGL((gate_kernel<F, L, V, true>), dim3((unsigned)gate_blocks(a.T, a.E)),
+                           dim3(256), (size_t)a.E * 8, stream, a);
+    else
+        hipLaunchKernelGGL((gate_kernel<F, L, V, false>), dim3((unsigned)all), dim3(256), 0,
+                           stream, a);
+    EP_HIP_CHECK(hipGetLastError());
+    return EP_OK;
+}
+
+template <typename F>
+int launch_gate(const GateArgs& a, bool stats, hipStream_t stream) {
+    const int E = a.E;
+#define EP_CALL(L, V) launch_gate_lv<F, L, V>(a, stats, stream)
+    EP_GATE_SIZES(EP_CALL);
+#undef EP_CALL
+}
+
+template <typename F, int L, int V>
+int launch_gate_back_lv(const GateBackArgs& a, hipStream_t stream) {
+    clear_hip_error();
+    hipLaunchKernelGGL((gate_back_kernel<F, L, V>), dim3((unsigned)ceil_div(a.T, 256 / L)),
+                       dim3(256), 0, stream, a);
+    EP_HIP_CHECK(hipGetLastError());
+    return EP_OK;
+}
+
+template <typename F>
+int launch_gate_back(const GateBackArgs& a, hipStream_t stream) {
+    const int E = a.E;
+#define EP_CALL(L, V) launch_gate_back_lv<F, L, V>(a, stream)
+    EP_GATE_SIZES(EP_CALL);
+#undef EP_CALL
+}
+}  // namespace
+
+extern "C" size_t ep_route_workspace_bytes(int32_t T, int32_t E) {
+    if (check_gate(T, E, 1) != EP_OK) return 0;
+    return gate_workspace(T, E);
+}
+
+extern "C" int ep_route(int32_t T, int32_t E, int32_t k, int32_t dtype, int32_t mode,
+                        const void* logits, const uint8_t* token_mask, int32_t* topk_idx,
+                        float* topk_w, int32_t* num_tokens_per_expert, int32_t* num_tokens,
+                        float* lse, float* balance_loss, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream) {
+    int v = check_gate(T, E, k);
+    if (v != EP_OK) return v;
+    if (dtype != EP_BF16 && dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    if (mode != EP_GATE_SOFTMAX && mode != EP_GATE_SOFTMAX_RENORM) return EP_ERR_INVALID_ARG;
+    const bool stats = num_tokens_per_expert || num_tokens || balance_loss;
+    if (stats && (!num_tokens_per_expert || !num_tokens || !balance_loss || !workspace))
+        return EP_ERR_INVALID_ARG;
+    if (stats && (workspace_bytes < gate_workspace(T, E) || ((uintptr_t)workspace & 15)))
+        return EP_ERR_INVALID_ARG;
+    if (T > 0 && (!logits || !topk_idx || !topk_w)) return EP_ERR_INVALID_ARG;
+    if (((uintptr_t)topk_idx | (uintptr_t)topk_w | (uintptr_t)lse |
+         (uintptr_t)num_tokens_per_expert | (uintptr_t)num_tokens | (uintptr_t)balance_loss) & 3)
+        return EP_ERR_INVALID_ARG;
+    if ((uintptr_t)logits & (dtype == EP_F32 ? 3 : 1)) return EP_ERR_INVALID_ARG;
+    if (T == 0 && !stats) return EP_OK;
+    const int64_t blocks = gate_blocks(T, E);
+    uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+    GateArgs a{};
+    a.logits = logits;
+    a.mask = token_mask;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.lse = lse;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.renorm = mode == EP_GATE_SOFTMAX_RENORM;
+    if (stats) {
+        a.part_p = reinterpret_cast<float*>(ws + 256 + sum_blocks(E) * 8);
+        a.part_n = reinterpret_cast<int32_t*>(a.part_p + blocks * E);
+        a.part_kept = a.part_n + blocks * E;
+    }
+    v = dtype == EP_F32 ? launch_gate<float>(a, stats, stream)
+                        : launch_gate<uint16_t>(a, stats, stream);
+    if (v != EP_OK || !stats) return v;
+    GateSumArgs b{};
+    b.part_p = a.part_p;
+    b.part_n = a.part_n;
+    b.part_kept = a.part_kept;
+    b.num_tokens_per_expert = num_tokens_per_expert;
+    b.num_tokens = num_tokens;
+    b.balance_loss = balance_loss;
+    b.part_loss = reinterpret_cast<double*>(ws + 256);
+    b.arrive = reinterpret_cast<uint32_t*>(ws);
+    b.blocks = (int32_t)blocks;
+    b.E = E;
+    b.k = k;
+    hipLaunchKernelGGL(gate_sum_kernel, dim3((unsigned)sum_blocks(E)), dim3(256), 0, stream, b);
+    EP_HIP_CHECK(hipGetLastError());
+    return EP_OK;
+}
+
+extern "C" int ep_route_backward(int32_t T, int32_t E, int32_t k, int32_t dtype, int32_t mode,
+                                 const void* logits, const uint8_t* token_mask,
+                                 const int32_t* topk_idx, const float* topk_w,
+                                 const int32_t* num_tokens_per_expert, const int32_t* num_tokens,
+                                 const float* lse, const float* grad_topk_w,
+                                 const float* grad_balance_loss, void* grad_logits,
+                                 hipStream_t stream) {
+    int v = check_gate(T, E, k);
+    if (v != EP_OK) return v;
+    if (dtype != EP_BF16 && dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    if (mode != EP_GATE_SOFTMAX && mode != EP_GATE_SOFTMAX_RENORM) return EP_ERR_INVALID_ARG;
+    if (T == 0) return EP_OK;
+    if (!logits || !lse || !grad_logits) return EP_ERR_INVALID_ARG;
+    if (grad_topk_w && (!topk_idx || !topk_w)) return EP_ERR_INVALID_ARG;
+    if (grad_balance_loss && (!num_tokens_per_expert || !num_tokens)) return EP_ERR_INVALID_ARG;
+    if (((uintptr_t)topk_idx | (uintptr_t)topk_w | (uintptr_t)lse | (uintptr_t)grad_topk_w |
+         (uintptr_t)num_tokens_per_expert | (uintptr_t)num_tokens |
+         (uintptr_t)grad_balance_loss) & 3)
+        return EP_ERR_INVALID_ARG;
+    if (((uintptr_t)logits | (uintptr_t)grad_logits) & (dtype == EP_F32 ? 3 : 1))
+        return EP_ERR_INVALID_ARG;
+    GateBackArgs a{};
+    a.logits = logits;
+    a.mask = token_mask;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.lse = lse;
+    a.num_tokens_per_expert = num_tokens_per_expert;
+    a.num_tokens = num_tokens;
+    a.grad_topk_w = grad_topk_w;
+    a.grad_balance_loss = grad_balance_loss;
+    a.grad_logits = grad_logits;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.renorm = mode == EP_GATE_SOFTMAX_RENORM;
+    return dtype == EP_F32 ? launch_gate_back<float>(a, stream)
+                           : launch_gate_back<uint16_t>(a, stream);
+}

@@ -82,6 +82,13 @@ enum ep_format {
                                   to a multiple of 128 bytes */
 };
 
+/* Element types of the operators that take more than one. */
+enum ep_dtype { EP_BF16 = 0, EP_F32 = 1 };
+
+/* Gate weights of a token's chosen experts: their softmax probabilities over
+ * all experts, or those divided by their sum over the chosen. */
+enum ep_gate { EP_GATE_SOFTMAX = 0, EP_GATE_SOFTMAX_RENORM = 1 };
+
 /* TransferCmd types (UCCL-EP s3.1) and atomic ops (s3.2). */
 enum { EP_CMD_WRITE = 1, EP_CMD_ATOMIC = 2 };
 enum { EP_ATOMIC_ADD = 1 };
@@ -355,6 +362,122 @@ int ep_dispatch_ll_fused(const ep_shape_t* shape, const void* x, const int32_t* 
 int ep_combine_ll(const ep_shape_t* shape, const void* y, int64_t y_rows,
                   const int32_t* topk_idx, const float* topk_w, const int32_t* expert_slot,
                   void* out, int32_t* dev_status, hipStream_t stream);
+
+/* ---- Around dispatch and combine ---------------------------------------------
+ * The operators that a mixture-of-experts layer has next to its exchange: the
+ * norm that makes its rows, the router that names their experts, and the
+ * experts' two products.  An "8-bit row" below is a row of
+ * EP_FMT_FP8_E4M3_B128 as the dispatch packs it: H e4m3 codes, H/128 float
+ * scales (a/448, a = max(max|v|, 1e-4) of the block), zero bytes up to
+ * ep_row_bytes; NaN and infinite elements as at ep_dispatch.  All tensors are
+ * contiguous; in- and outputs must not overlap except where a call says so. */
+
+/* Root-mean-square norm of T rows of H values with the residual's addition.
+ *   r = bf16(x + residual)  (x itself without a residual)
+ *   y = r * rsqrt(mean(r^2) + eps) * weight
+ *   x, residual   bf16 [T,H]; residual may be NULL
+ *   weight        float [H]
+ *   residual_out  bf16 [T,H]: r, or NULL (NULL without a residual)
+ *   y             bf16 [T,H], or NULL
+ *   rows          [T, ep_row_bytes(H, EP_FMT_FP8_E4M3_B128)]: y as 8-bit rows
+ *                 (quantised from float, not from the bf16 y), or NULL;
+ *                 needs H % 128 == 0.  One of y and rows at least.
+ *   rstd          float [T]: rsqrt(mean(r^2) + eps), for the backward, or NULL
+ * 8 <= H <= 32768, H % 8 == 0; eps >= 0 and finite.  residual_out or y may be
+ * x or residual themselves (a row is read before it is written), but not the
+ * same one.  Every pointer 16-byte aligned, rstd 4-byte. */
+int ep_rmsnorm(int32_t T, int32_t H, const void* x, const void* residual, const float* weight,
+               float eps, void* residual_out, void* y, void* rows, float* rstd,
+               hipStream_t stream);
+
+/* Its backward.  With h = r * rstd and g = grad_y * weight:
+ *   grad_x      = rstd * (g - h * mean(g * h)) + grad_residual   bf16 [T,H]
+ *                 (the gradient of x and of residual alike)
+ *   grad_weight = sum over the rows of grad_y * h                float [H]
+ *   r             bf16 [T,H]: residual_out of the forward call (x without one)
+ *   grad_y        bf16 [T,H]; an 8-bit output's gradient is taken as y's
+ *   grad_residual bf16 [T,H]: the gradient of residual_out, or NULL
+ *   workspace     ep_rmsnorm_workspace_bytes(T, H) bytes, need not be zeroed;
+ *                 calls that overlap in time need one each
+ * The sums run in a fixed order.  grad_x may be grad_y or grad_residual
+ * itself.  T = 0 makes grad_weight zero. */
+size_t ep_rmsnorm_workspace_bytes(int32_t T, int32_t H);
+int ep_rmsnorm_backward(int32_t T, int32_t H, const void* r, const float* weight,
+                        const float* rstd, const void* grad_y, const void* grad_residual,
+                        void* grad_x, float* grad_weight, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/* The router: each token's experts and gate weights, as the dispatch calls
+ * take them, and the balance loss.
+ *   logits     [T,E], dtype EP_BF16 or EP_F32
+ *   token_mask uint8 [T], 0 = a padded token (its logits are not looked at), or
+ *              NULL
+ *   topk_idx   int32 [T,k]: the experts of the k largest logits, descending,
+ *              ties to the lowest expert; -1 for every choice of a padded token,
+ *              and for choices beyond the logits that are neither -inf nor NaN
+ *   topk_w     float [T,k]: p = softmax(logits) of the chosen
+ *              (EP_GATE_SOFTMAX), or p divided by its sum over the chosen
+ *              (EP_GATE_SOFTMAX_RENORM); 0 where topk_idx is -1
+ *   lse        float [T]: log of the sum of exp(logits), for the backward (0 for
+ *              a padded token), or NULL
+ * and, all three or none (NULL):
+ *   num_tokens_per_expert int32 [E]: choices of each expert, c_e
+ *   num_tokens            int32 [1]: tokens that are not padded, n
+ *   balance_loss          float [1]: E * sum_e (c_e / (n k)) * (sum_t p[t,e] / n)
+ *              over those tokens; 0 if there is none
+ *   workspace  ep_route_workspace_bytes(T, E) bytes, zero-filled once before
+ *              its first use, left consistent by every call; calls that overlap
+ *              in time need one each (needed for these three only)
+ * A NaN or +inf logit of a token that is not padded makes its weights, its lse
+ * and the loss NaN.  1 <= k <= min(E, 32), E <= 4096.  The sums run in a fixed
+ * order. */
+size_t ep_route_workspace_bytes(int32_t T, int32_t E);
+int ep_route(int32_t T, int32_t E, int32_t k, int32_t dtype, int32_t mode, const void* logits,
+             const uint8_t* token_mask, int32_t* topk_idx, float* topk_w,
+             int32_t* num_tokens_per_expert, int32_t* num_tokens, float* lse,
+             float* balance_loss, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of the logits, [T,E] in their dtype, from those of the gate weights
+ * (float [T,k], or NULL: zero) and of the balance loss (float [1] on the
+ * device, or NULL: zero); the other arguments are the forward call's in- and
+ * outputs (what belongs to a NULL gradient may be NULL).  The choices and
+ * counts are constants.  A padded token's row is zero.  grad_logits may be
+ * logits itself. */
+int ep_route_backward(int32_t T, int32_t E, int32_t k, int32_t dtype, int32_t mode,
+                      const void* logits, const uint8_t* token_mask, const int32_t* topk_idx,
+                      const float* topk_w, const int32_t* num_tokens_per_expert,
+                      const int32_t* num_tokens, const float* lse, const float* grad_topk_w,
+                      const float* grad_balance_loss, void* grad_logits, hipStream_t stream);
+
+/* Product of 8-bit rows, grouped by expert, with their experts' weights.
+ *   rows         [M, ep_row_bytes(K, EP_FMT_FP8_E4M3_B128)] 8-bit rows
+ *   group_offset int32 [G+1], on the device: expert g's rows are
+ *                [group_offset[g], group_offset[g+1]); expert_offset of a
+ *                per-expert layout, or any G + 1 consecutive words of it (one
+ *                rank's experts).  An expert may have no rows.
+ *   w            e4m3 codes [G,N,K];  w_scale float [G, ceil(N/128), K/128]:
+ *                weight (n,k) is its code times w_scale[n/128, k/128]
+ *   out          bf16 [M,N]: out[m,:] = rows[m] times w[g] transposed.  Rows of
+ *                no expert are left as they were.
+ * K % 128 == 0, N % 8 == 0, G <= 4096, M < 2^31; with G = 1 it is a plain
+ * matrix product.  Sums are float, blocks of 128 products one matrix
+ * instruction.  The weights are a serving form: they have no gradient.
+ * Device errors: EP_ERR_CAPACITY if an offset exceeds M (rows from M on are
+ * skipped), EP_ERR_INVALID_ARG if one is negative or they decrease (outputs
+ * are then unspecified, nothing outside out is written).
+ * rows, w and out 16-byte aligned. */
+int ep_expert_product(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
+                      const int32_t* group_offset, const void* w, const float* w_scale, void* out,
+                      int32_t* dev_status, hipStream_t stream);
+
+/* The first product of a gated expert: w is [G,2F,K], F gates' rows and then F
+ * ups', w_scale [G, 2F/128, K/128]; with y = rows times w transposed,
+ *   out_rows[m] = silu(y[m,:F]) * y[m,F:]  as an 8-bit row, [M,
+ *                 ep_row_bytes(F, EP_FMT_FP8_E4M3_B128)], quantised from float,
+ * which ep_expert_product takes as it is.  F % 128 == 0; the rest as there. */
+int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, const void* rows,
+                      const int32_t* group_offset, const void* w, const float* w_scale,
+                      void* out_rows, int32_t* dev_status, hipStream_t stream);
 
 /* ---- TransferCmd ring (UCCL-EP s2.2, s2.3, s5.2) ---------------------------
  * `channels` FIFOs of `depth` slots each; a producer blocks while
