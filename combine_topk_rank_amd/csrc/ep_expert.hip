@@ -17,6 +17,8 @@
 // and drops what falls 13 bits below it, 1.4e-5 of a random sum; between those
 // eights and between blocks the sum is float.)
 
+#include <type_traits>
+
 #include "ep_rows8.h"
 
 namespace ep {
@@ -35,7 +37,7 @@ struct ExpertArgs {
     int32_t G, N, K, row_bytes, out_bytes, n_tiles;
 };
 
-// The rows of tile `tile` of `bm` rows, tiles counted over the groups in order.
+// The rows of a tile of `bm` rows, tiles counted over the groups in order.
 struct RowTile {
     int32_t g;        // group; -1: no such tile
     int64_t first;    // first row of the tile
@@ -228,10 +230,304 @@ __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
     }
 }
 
+// ---- Many rows a group ----------------------------------------------------------
+// A workgroup of eight wavefronts has 256 weight rows (for the gate: the 128
+// gates and 128 ups of one output block) and up to 256 rows of one group.  One
+// block of K of both, 64 KB, goes straight from memory to LDS while the
+// wavefronts work on the block before it: 2 x 64 of the 160 KB.  A wavefront
+// has 128 weight rows x 64 rows, 32 MFMAs a block from 12 operand tiles, so
+// the LDS gives 196 KB a block in 1536 cycles next to 2048 of the matrix units.
+constexpr int kBigRows = 256;      // weight rows, and rows, of a workgroup
+constexpr int kBigThreads = 512;
+constexpr int kOperandBytes = kBigRows * kScaleBlock;
+constexpr int kStageBytes = 2 * kOperandBytes;
+
+typedef __attribute__((address_space(3))) void* LdsPtr;
+
+// Sixteen bytes a lane from offset `lane_at` + `at` of a buffer to LDS: 64 lanes
+// to 1 KB from `lds` on; `at` and `lds` are the same for the wavefront.
+__device__ inline void to_lds(__amdgpu_buffer_rsrc_t p, uint32_t lane_at, uint32_t at,
+                              uint8_t* lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(p, (LdsPtr)lds, 16, (int)lane_at, (int)at, 0, 0);
+}
+
+__device__ inline f32x4 pick(bool first, f32x4 a, f32x4 b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = first ? a[i] : b[i];
+    return a;
+}
+
+// Tiles of all groups.
+__device__ inline int64_t count_tiles(const int32_t* off, int G, int64_t M, int bm) {
+    int64_t all = 0;
+    for (int g0 = 0; g0 < G; g0 += kWave) {
+        const int g = g0 + lane_id();
+        int t = 0;
+        if (g < G) {
+            const int64_t n = clamp_row(off[g + 1], M) - clamp_row(off[g], M);
+            t = n > 0 ? (int)((n + bm - 1) / bm) : 0;
+        }
+#pragma unroll
+        for (int o = 1; o < kWave; o *= 2) t += __shfl_xor(t, o);
+        all += bcast(t, 0);
+    }
+    return all;
+}
+
+// Which tile a workgroup takes.  Workgroups go to the eight XCDs in turn: each
+// XCD gets one run of the tiles, ordered so that the 32 it has at a time are 4
+// row tiles x 8 column tiles, whose operands its L2 shares.
+struct TilePlace {
+    int64_t m;      // row tile; -1: none left
+    int n;          // column tile
+};
+
+__device__ inline TilePlace place_tile(int64_t row_tiles, int n_tiles) {
+    const int64_t all = row_tiles * n_tiles;
+    const int xcd = (int)(blockIdx.x % 8u);
+    const int64_t slot = blockIdx.x / 8u, per = all / 8, extra = all % 8;
+    if (slot >= per + (xcd < extra)) return {-1, 0};
+    const int64_t at = xcd * per + (xcd < extra ? xcd : extra) + slot;
+    const int64_t band = at / (4 * n_tiles), in = at - band * 4 * n_tiles;
+    const int64_t left = row_tiles - band * 4;
+    const int64_t rows = left < 4 ? left : 4;
+    return {band * 4 + in % rows, (int)(in / rows)};
+}
+
+template <bool GATE>
+__global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[2 * kStageBytes];
+    if (blockIdx.x == 0) check_groups(a);
+    const TilePlace place =
+        place_tile(count_tiles(a.group_offset, a.G, a.M, kBigRows), a.n_tiles);
+    if (place.m < 0) return;
+    const int nt = place.n;
+    const RowTile tile = find_tile(a.group_offset, a.G, a.M, place.m, kBigRows);
+    if (tile.g < 0) return;
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    // wavefronts 2 wm and 2 wm + 1 share rows: where a tile has few rows, those
+    // without any idle on every SIMD alike
+    const int wn = wave % 2, wm = wave / 2;
+    const int nb = a.K / kScaleBlock;
+    const int F = a.N / 2;
+
+    // What this lane copies: rows wave * 32 + i * 8 + lane / 8 of both operands.
+    // Sixteen-byte chunk c of row r sits at chunk c ^ (r / 2 % 8) of its 128
+    // bytes, so that 16 rows' reads of one chunk meet all 64 banks once.  Rows
+    // behind the last repeat it; their results are not stored.
+    const int n0 = GATE ? (wave < 4 ? 0 : F - 128) + nt * 128 : nt * kBigRows;
+    const uint8_t* const wbase = a.w + ((int64_t)tile.g * a.N + n0) * a.K;
+    const uint8_t* const xbase = a.rows + tile.first * a.row_bytes;
+    // 256 rows of at most 2^20 + 2^15 bytes each: offsets stay below 2^31
+    const __amdgpu_buffer_rsrc_t wbuf = buffer_rsrc(const_cast<uint8_t*>(wbase), kBigRows * a.K);
+    const __amdgpu_buffer_rsrc_t xbuf =
+        buffer_rsrc(const_cast<uint8_t*>(xbase), tile.count * a.row_bytes);
+    uint32_t ow[4], ox[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = wave * 32 + i * 8 + lane / 8;
+        const int c = (lane % 8) ^ (r / 2 % 8);
+        const int n = n0 + r < a.N ? r : a.N - 1 - n0;
+        ow[i] = (uint32_t)n * (uint32_t)a.K + c * 16;
+        ox[i] = (uint32_t)(r < tile.count ? r : tile.count - 1) * (uint32_t)a.row_bytes + c * 16;
+    }
+    const auto fetch = [&](int b) {
+        uint8_t* l = s_mem + (b & 1) * kStageBytes + wave * 4096;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            to_lds(wbuf, ow[i], b * kScaleBlock, l + i * 1024);
+            to_lds(xbuf, ox[i], b * kScaleBlock, l + kOperandBytes + i * 1024);
+        }
+    };
+
+    f32x4 acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int r = lane % 16, g = lane / 16;
+
+    fetch(0);
+    if (wm * 64 >= tile.count) {
+        // no rows of its own: this wavefront only copies
+        for (int b = 0; b < nb; ++b) {
+            wait_vm();
+            __syncthreads();
+            if (b + 1 < nb) fetch(b + 1);
+        }
+    } else {
+        // scales: this lane's four rows, this wavefront's block of weight rows
+        uint32_t osx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int m = wm * 64 + j * 16 + r;
+            osx[j] = (uint32_t)(m < tile.count ? m : tile.count - 1) * (uint32_t)a.row_bytes + a.K;
+        }
+        const int scale_rows = (a.N + 127) / 128;
+        int sr = GATE ? (wn ? F / 128 : 0) + nt : nt * 2 + wn;
+        sr = sr < scale_rows ? sr : scale_rows - 1;
+        const float* psw = a.w_scale + ((int64_t)tile.g * scale_rows + sr) * nb;
+        float sx[4], sw, s[4], sn[4], sp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const auto scales = [&](int b) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sx[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(xbuf, osx[j], 4 * b, 0));
+            sw = psw[b];
+        };
+        const int at0 = r * 128 + ((g ^ (r / 2)) * 16), at1 = at0 ^ 64;
+        const auto wtile = [&](int b, int i) {
+            const uint8_t* l = s_mem + (b & 1) * kStageBytes + wn * 16384 + i * 2048;
+            return join(load16(l + at0), load16(l + at1));
+        };
+        const auto xtile = [&](int b, int j) {
+            const uint8_t* l =
+                s_mem + (b & 1) * kStageBytes + kOperandBytes + wm * 8192 + j * 2048;
+            return join(load16(l + at0), load16(l + at1));
+        };
+
+        scales(0);
+        wait_vm();
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = sx[j] * sw;
+        if (nb > 1) {
+            scales(1);
+            fetch(1);
+        }
+        // One block of K: 32 MFMAs q = 4 i + j, each followed by the scaled sum
+        // of the one two before it, so that neither unit waits for the other.
+        // Weight tiles are read two ahead.  When the last of this block's LDS
+        // reads is back (i = 6), the wavefronts meet: block b + 1 has arrived
+        // for all, and block b's stage is free for block b + 2; the MFMAs left
+        // cover the meeting and the first reads of block b + 1.
+        i32x8 w[3], x[4];
+        f32x4 t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = xtile(0, j);
+            t[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        w[0] = wtile(0, 0);
+        // left: blocks after this one, 2 for two or more
+        const auto block = [&](int b, auto left) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i == 0) w[1] = wtile(b, 1);
+                if (i < 6) w[(i + 2) % 3] = wtile(b, i + 2);
+                if constexpr (left.value > 0) {
+                    if (i == 6) {
+                        wait_vm();
+                        __syncthreads();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sn[j] = sx[j] * sw;
+                        if constexpr (left.value > 1) {
+                            scales(b + 2);
+                            fetch(b + 2);
+                        }
+                    }
+                    if (i == 7) w[0] = wtile(b + 1, 0);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int q = 4 * i + j, p = (q + 30) % 32;
+                    __builtin_amdgcn_sched_barrier(0);
+                    t[q % 4] = mfma16(w[i % 3], x[j]);
+                    acc[p / 4][p % 4] =
+                        fma4(t[p % 4], q < 2 ? sp[p % 4] : s[p % 4], acc[p / 4][p % 4]);
+                    if constexpr (left.value > 0)
+                        if (i == 7) x[j] = xtile(b + 1, j);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sp[j] = s[j];
+                s[j] = sn[j];
+            }
+        };
+        for (int b = 0; b < nb - 2; ++b) block(b, std::integral_constant<int, 2>{});
+        if (nb > 1) block(nb - 2, std::integral_constant<int, 1>{});
+        block(nb - 1, std::integral_constant<int, 0>{});
+#pragma unroll
+        for (int p = 30; p < 32; ++p)
+            acc[p / 4][p % 4] = fma4(t[p % 4], sp[p % 4], acc[p / 4][p % 4]);
+    }
+
+    if constexpr (!GATE) {
+        // lane: columns 4 g .. 4 g + 3 of each 16, one row of each 16
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int m = wm * 64 + j * 16 + r;
+            if (m >= tile.count) continue;
+            uint8_t* row = a.out + (tile.first + m) * a.out_bytes;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = nt * kBigRows + wn * 128 + i * 16 + g * 4;
+                if (c < a.N)
+                    *reinterpret_cast<u32x2*>(row + 2 * c) =
+                        u32x2{bf16_pack(acc[i][j][0], acc[i][j][1]),
+                              bf16_pack(acc[i][j][2], acc[i][j][3])};
+            }
+        }
+    } else {
+        // The gates' wavefront hands the ups' the second half of its rows and
+        // takes the first half of the ups' rows: 16 KB each way a pair, in the
+        // lanes' own order.
+        __syncthreads();
+        f32x4* const mine = reinterpret_cast<f32x4*>(s_mem) + wave * 1024;
+        f32x4* const other = reinterpret_cast<f32x4*>(s_mem) + (wave ^ 1) * 1024;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                mine[(i * 2 + j) * 64 + lane] = pick(wn, acc[i][j], acc[i][j + 2]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float h[8][4];
+            float am = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const f32x4 got = other[(i * 2 + j) * 64 + lane];
+                const f32x4 own = pick(wn, acc[i][j + 2], acc[i][j]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    h[i][q] = silu_mul(wn ? got[q] : own[q], wn ? own[q] : got[q]);
+                    am = fmaxf(am, fabsf(h[i][q]));
+                }
+            }
+            am = fmaxf(am, __shfl_xor(am, 16));
+            am = fmaxf(am, __shfl_xor(am, 32));
+            am = fmaxf(am, kAmaxMin);
+            const int m = wm * 64 + (wn * 2 + j) * 16 + r;
+            if (m < tile.count) {
+                uint8_t* row = a.out + (tile.first + m) * a.out_bytes;
+                const float inv = kFp8Max / am;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float p[8] = {h[i][0], h[i][1], h[i][2], h[i][3],
+                                        h[i + 1][0], h[i + 1][1], h[i + 1][2], h[i + 1][3]};
+                    const u32x2 code = fp8_pack8(p, inv);
+                    *reinterpret_cast<uint32_t*>(row + nt * 128 + i * 16 + g * 4) = code.x;
+                    *reinterpret_cast<uint32_t*>(row + nt * 128 + i * 16 + 16 + g * 4) = code.y;
+                }
+                if (g == 0) *reinterpret_cast<float*>(row + F + 4 * nt) = am / kFp8Max;
+                if (nt == F / 128 - 1)
+                    for (int o = F + F / 32 + 4 * g; o < a.out_bytes; o += 16)
+                        *reinterpret_cast<uint32_t*>(row + o) = 0u;
+            }
+        }
+    }
+}
+
+// A tile's 256 rows stay within 32-bit offsets.
+constexpr int kMaxK8 = 1 << 20;
+
 // Shared by both calls: shapes whose indexes the kernels hold in 32 bits.
 int check_expert(int32_t G, int64_t M, int32_t N, int32_t K) {
     if (G < 1 || G > kMaxE || M < 0 || M >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
-    if (K < kScaleBlock || K % kScaleBlock != 0 || K > kMaxH) return EP_ERR_INVALID_ARG;
+    if (K < kScaleBlock || K % kScaleBlock != 0 || K > kMaxK8) return EP_ERR_INVALID_ARG;
     if (N < 8 || N % 8 != 0 || N > kMaxH) return EP_ERR_INVALID_ARG;
     return EP_OK;
 }
@@ -268,9 +564,10 @@ int expert_args(ExpertArgs& a, int32_t G, int64_t M, int32_t N, int32_t K, const
     return EP_OK;
 }
 
-// Workgroups of a launch: column tiles x the row tiles that there can be.
-int grid_of(const ExpertArgs& a, int bm, unsigned* blocks) {
-    const int64_t n = max_tiles(a.M, a.G, bm) * a.n_tiles;
+// Workgroups of a launch: column tiles x the row tiles that there can be,
+// rounded up to a multiple of `step`.
+int grid_of(const ExpertArgs& a, int bm, int step, unsigned* blocks) {
+    const int64_t n = ceil_div(max_tiles(a.M, a.G, bm) * a.n_tiles, step) * step;
     if (n >= ((int64_t)1 << 31)) {
         record_error("expert product: more than 2^31 tiles");
         return EP_ERR_INVALID_ARG;
@@ -279,10 +576,10 @@ int grid_of(const ExpertArgs& a, int bm, unsigned* blocks) {
     return EP_OK;
 }
 
-#define EP_LAUNCH_TILES(KERNEL, BM, THREADS)                                               \
+#define EP_LAUNCH_TILES(KERNEL, BM, THREADS, STEP)                                            \
     do {                                                                                   \
         unsigned blocks = 0;                                                               \
-        const int v_ = grid_of(a, BM, &blocks);                                            \
+        const int v_ = grid_of(a, BM, STEP, &blocks);                                      \
         if (v_ != EP_OK) return v_;                                                        \
         clear_hip_error();                                                                 \
         hipLaunchKernelGGL((KERNEL), dim3(blocks), dim3(THREADS), 0, stream, a);           \
@@ -303,9 +600,13 @@ extern "C" int ep_expert_product(int32_t G, int64_t M, int32_t N, int32_t K, con
     a.out_bytes = 2 * N;
     a.n_tiles = (int32_t)ceil_div(N, 16);
     const int64_t per = ceil_div(M, G);   // rows a group, were they even
-    if (per <= 16) EP_LAUNCH_TILES(product_small_kernel<1>, 16, 256);
-    if (per <= 32) EP_LAUNCH_TILES(product_small_kernel<2>, 32, 256);
-    EP_LAUNCH_TILES(product_small_kernel<4>, 64, 256);
+    if (per > 64) {
+        a.n_tiles = (int32_t)ceil_div(N, kBigRows);
+        EP_LAUNCH_TILES(product_big_kernel<false>, kBigRows, kBigThreads, 8);
+    }
+    if (per <= 16) EP_LAUNCH_TILES(product_small_kernel<1>, 16, 256, 1);
+    if (per <= 32) EP_LAUNCH_TILES(product_small_kernel<2>, 32, 256, 1);
+    EP_LAUNCH_TILES(product_small_kernel<4>, 64, 256, 1);
 }
 
 extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, const void* rows,
@@ -321,7 +622,8 @@ extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, con
     a.out_bytes = (int32_t)row_bytes(F, EP_FMT_FP8_E4M3_B128);
     a.n_tiles = F / kScaleBlock;
     const int64_t per = ceil_div(M, G);
-    if (per <= 16) EP_LAUNCH_TILES(gate_up_small_kernel<1>, 16, 1024);
-    if (per <= 32) EP_LAUNCH_TILES(gate_up_small_kernel<2>, 32, 1024);
-    EP_LAUNCH_TILES(gate_up_small_kernel<4>, 64, 1024);
+    if (per > 64) EP_LAUNCH_TILES(product_big_kernel<true>, kBigRows, kBigThreads, 8);
+    if (per <= 16) EP_LAUNCH_TILES(gate_up_small_kernel<1>, 16, 1024, 1);
+    if (per <= 32) EP_LAUNCH_TILES(gate_up_small_kernel<2>, 32, 1024, 1);
+    EP_LAUNCH_TILES(gate_up_small_kernel<4>, 64, 1024, 1);
 }

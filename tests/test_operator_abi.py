@@ -110,7 +110,7 @@ def gate_up(L, G=2, M=4, F=128, K=128, rows=A, off=A, w=A, ws=A, out=A, st=A):
 
 
 COMMON = [dict(G=0), dict(G=4097), dict(M=-1), dict(M=1 << 31), dict(K=0), dict(K=64), dict(K=192),
-          dict(K=(1 << 24) + 128), dict(rows=None), dict(off=None), dict(w=None), dict(ws=None),
+          dict(K=(1 << 20) + 128), dict(rows=None), dict(off=None), dict(w=None), dict(ws=None),
           dict(out=None), dict(st=None), dict(rows=A + 8), dict(w=A + 8), dict(out=A + 8),
           dict(off=A + 2), dict(ws=A + 2), dict(st=A + 1)]
 
