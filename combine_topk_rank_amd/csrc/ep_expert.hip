@@ -232,15 +232,16 @@ __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
 
 // ---- Many rows a group ----------------------------------------------------------
 // A workgroup of eight wavefronts has 256 weight rows (for the gate: the 128
-// gates and 128 ups of one output block) and up to 256 rows of one group.  One
-// block of K of both, 64 KB, goes straight from memory to LDS while the
-// wavefronts work on the block before it: 2 x 64 of the 160 KB.  A wavefront
-// has 128 weight rows x 64 rows, 32 MFMAs a block from 12 operand tiles, so
-// the LDS gives 196 KB a block in 1536 cycles next to 2048 of the matrix units.
+// gates and 128 ups of one output block) and up to 256 rows of one group.  The
+// blocks of K of both, 32 KB each, go straight from memory to LDS ahead of
+// their use: three blocks of weights and two of rows fill its 160 KB.  A
+// wavefront has 128 weight rows x 64 rows, 32 MFMAs a block from 12 operand
+// tiles, so the LDS gives 196 KB a block in 1536 cycles next to 2048 of the
+// matrix units.
 constexpr int kBigRows = 256;      // weight rows, and rows, of a workgroup
 constexpr int kBigThreads = 512;
 constexpr int kOperandBytes = kBigRows * kScaleBlock;
-constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kRowsAt = 3 * kOperandBytes;      // LDS: three blocks of weights, two of rows
 
 typedef __attribute__((address_space(3))) void* LdsPtr;
 
@@ -249,6 +250,19 @@ typedef __attribute__((address_space(3))) void* LdsPtr;
 __device__ inline void to_lds(__amdgpu_buffer_rsrc_t p, uint32_t lane_at, uint32_t at,
                               uint8_t* lds) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(p, (LdsPtr)lds, 16, (int)lane_at, (int)at, 0, 0);
+}
+
+// Waits until at most N of the wavefront's copies are under way and its LDS
+// reads are done, then for the other wavefronts.  (__syncthreads would wait for
+// all the copies.)
+template <int N>
+__device__ inline void meet() {
+    asm volatile("" ::: "memory");
+    // gfx9 encoding: vmcnt in bits 3:0 and 15:14, expcnt 6:4 at its maximum,
+    // lgkmcnt 11:8 zero
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x70);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 __device__ inline f32x4 pick(bool first, f32x4 a, f32x4 b) {
@@ -296,7 +310,7 @@ __device__ inline TilePlace place_tile(int64_t row_tiles, int n_tiles) {
 
 template <bool GATE>
 __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs a) {
-    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[2 * kStageBytes];
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[5 * kOperandBytes];
     if (blockIdx.x == 0) check_groups(a);
     const TilePlace place =
         place_tile(count_tiles(a.group_offset, a.G, a.M, kBigRows), a.n_tiles);
@@ -331,13 +345,14 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs 
         ow[i] = (uint32_t)n * (uint32_t)a.K + c * 16;
         ox[i] = (uint32_t)(r < tile.count ? r : tile.count - 1) * (uint32_t)a.row_bytes + c * 16;
     }
-    const auto fetch = [&](int b) {
-        uint8_t* l = s_mem + (b & 1) * kStageBytes + wave * 4096;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            to_lds(wbuf, ow[i], b * kScaleBlock, l + i * 1024);
-            to_lds(xbuf, ox[i], b * kScaleBlock, l + kOperandBytes + i * 1024);
-        }
+    // one of the four parts of this wavefront's copy of block b
+    const auto fetch_w = [&](int b, int i) {
+        to_lds(wbuf, ow[i], b * kScaleBlock,
+               s_mem + b % 3 * kOperandBytes + wave * 4096 + i * 1024);
+    };
+    const auto fetch_x = [&](int b, int i) {
+        to_lds(xbuf, ox[i], b * kScaleBlock,
+               s_mem + kRowsAt + (b & 1) * kOperandBytes + wave * 4096 + i * 1024);
     };
 
     f32x4 acc[8][4];
@@ -347,13 +362,38 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs 
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int r = lane % 16, g = lane / 16;
 
-    fetch(0);
+    // Copies are spread over the work, one an i, in this order: in block b's
+    // i = 0, 1 the second half of rows b + 1, in i = 2 .. 5 weights b + 2, then,
+    // behind the meeting, scales b + 2 and in i = 6, 7 the first half of rows
+    // b + 2.  The meeting waits for all but weights b + 2.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        fetch_w(0, i);
+        fetch_x(0, i);
+    }
     if (wm * 64 >= tile.count) {
         // no rows of its own: this wavefront only copies
-        for (int b = 0; b < nb; ++b) {
-            wait_vm();
-            __syncthreads();
-            if (b + 1 < nb) fetch(b + 1);
+        if (nb > 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fetch_w(1, i);
+            fetch_x(1, 0);
+            fetch_x(1, 1);
+            meet<6>();
+        } else {
+            meet<0>();
+        }
+        for (int b = 0; b < nb - 1; ++b) {
+            fetch_x(b + 1, 2);
+            fetch_x(b + 1, 3);
+            if (b + 2 < nb) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fetch_w(b + 2, i);
+                meet<4>();
+                fetch_x(b + 2, 0);
+                fetch_x(b + 2, 1);
+            } else {
+                meet<0>();
+            }
         }
     } else {
         // scales: this lane's four rows, this wavefront's block of weight rows
@@ -376,30 +416,37 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs 
         };
         const int at0 = r * 128 + ((g ^ (r / 2)) * 16), at1 = at0 ^ 64;
         const auto wtile = [&](int b, int i) {
-            const uint8_t* l = s_mem + (b & 1) * kStageBytes + wn * 16384 + i * 2048;
+            const uint8_t* l = s_mem + b % 3 * kOperandBytes + wn * 16384 + i * 2048;
             return join(load16(l + at0), load16(l + at1));
         };
         const auto xtile = [&](int b, int j) {
             const uint8_t* l =
-                s_mem + (b & 1) * kStageBytes + kOperandBytes + wm * 8192 + j * 2048;
+                s_mem + kRowsAt + (b & 1) * kOperandBytes + wm * 8192 + j * 2048;
             return join(load16(l + at0), load16(l + at1));
         };
 
         scales(0);
-        wait_vm();
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = sx[j] * sw;
         if (nb > 1) {
+            const float sx0[4] = {sx[0], sx[1], sx[2], sx[3]}, sw0 = sw;
             scales(1);
-            fetch(1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fetch_w(1, i);
+            fetch_x(1, 0);
+            fetch_x(1, 1);
+            meet<11>();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = sx0[j] * sw0;
+        } else {
+            meet<0>();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = sx[j] * sw;
         }
         // One block of K: 32 MFMAs q = 4 i + j, each followed by the scaled sum
         // of the one two before it, so that neither unit waits for the other.
         // Weight tiles are read two ahead.  When the last of this block's LDS
         // reads is back (i = 6), the wavefronts meet: block b + 1 has arrived
-        // for all, and block b's stage is free for block b + 2; the MFMAs left
-        // cover the meeting and the first reads of block b + 1.
+        // for all, and block b's places are free; the MFMAs left cover the
+        // meeting and the first reads of block b + 1.
         i32x8 w[3], x[4];
         f32x4 t[4];
 #pragma unroll
@@ -415,16 +462,17 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs 
                 if (i == 0) w[1] = wtile(b, 1);
                 if (i < 6) w[(i + 2) % 3] = wtile(b, i + 2);
                 if constexpr (left.value > 0) {
+                    if (i < 2) fetch_x(b + 1, i + 2);
+                    if constexpr (left.value > 1)
+                        if (i >= 2 && i < 6) fetch_w(b + 2, i - 2);
                     if (i == 6) {
-                        wait_vm();
-                        __syncthreads();
+                        meet<(left.value > 1 ? 4 : 0)>();
 #pragma unroll
                         for (int j = 0; j < 4; ++j) sn[j] = sx[j] * sw;
-                        if constexpr (left.value > 1) {
-                            scales(b + 2);
-                            fetch(b + 2);
-                        }
+                        if constexpr (left.value > 1) scales(b + 2);
                     }
+                    if constexpr (left.value > 1)
+                        if (i >= 6) fetch_x(b + 2, i - 6);
                     if (i == 7) w[0] = wtile(b + 1, 0);
                 }
 #pragma unroll
