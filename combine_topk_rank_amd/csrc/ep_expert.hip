@@ -231,15 +231,17 @@ __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
 }
 
 // ---- Many rows a group ----------------------------------------------------------
-// A workgroup of eight wavefronts has 256 weight rows (for the gate: the 128
-// gates and 128 ups of one output block) and up to 256 rows of one group.  The
-// blocks of K of both, 32 KB each, go straight from memory to LDS ahead of
-// their use: three blocks of weights and two of rows fill its 160 KB.  A
+// A workgroup of eight wavefronts, one a CU, works through its share of tiles:
+// 256 weight rows (for the gate: the 128 gates and 128 ups of one output block)
+// x up to 256 rows of one group.  The blocks of K of both, 32 KB each, go
+// straight from memory to LDS ahead of their use, two blocks ahead and on into
+// the next tile: three blocks of weights and two of rows fill the 160 KB.  A
 // wavefront has 128 weight rows x 64 rows, 32 MFMAs a block from 12 operand
 // tiles, so the LDS gives 196 KB a block in 1536 cycles next to 2048 of the
 // matrix units.
-constexpr int kBigRows = 256;      // weight rows, and rows, of a workgroup
+constexpr int kBigRows = 256;      // weight rows, and rows, of a tile
 constexpr int kBigThreads = 512;
+constexpr int kBigGrid = 256;      // CUs of the GPU: one workgroup fills a CU's LDS
 constexpr int kOperandBytes = kBigRows * kScaleBlock;
 constexpr int kRowsAt = 3 * kOperandBytes;      // LDS: three blocks of weights, two of rows
 
@@ -252,23 +254,17 @@ __device__ inline void to_lds(__amdgpu_buffer_rsrc_t p, uint32_t lane_at, uint32
     __builtin_amdgcn_raw_ptr_buffer_load_lds(p, (LdsPtr)lds, 16, (int)lane_at, (int)at, 0, 0);
 }
 
-// Waits until at most N of the wavefront's copies are under way and its LDS
-// reads are done, then for the other wavefronts.  (__syncthreads would wait for
-// all the copies.)
-template <int N>
+// Waits until at most VM of the wavefront's memory operations and LDS of its
+// LDS reads are under way (each kind ends in its order), then for the other
+// wavefronts.  (__syncthreads would wait for all the copies.)
+template <int VM, int LDS>
 __device__ inline void meet() {
     asm volatile("" ::: "memory");
     // gfx9 encoding: vmcnt in bits 3:0 and 15:14, expcnt 6:4 at its maximum,
-    // lgkmcnt 11:8 zero
-    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x70);
+    // lgkmcnt 11:8
+    __builtin_amdgcn_s_waitcnt((VM & 15) | (VM >> 4 << 14) | 0x70 | LDS << 8);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-}
-
-__device__ inline f32x4 pick(bool first, f32x4 a, f32x4 b) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = first ? a[i] : b[i];
-    return a;
 }
 
 // Tiles of all groups.
@@ -288,285 +284,332 @@ __device__ inline int64_t count_tiles(const int32_t* off, int G, int64_t M, int 
     return all;
 }
 
-// Which tile a workgroup takes.  Workgroups go to the eight XCDs in turn: each
-// XCD gets one run of the tiles, ordered so that the 32 it has at a time are 4
-// row tiles x 8 column tiles, whose operands its L2 shares.
-struct TilePlace {
-    int64_t m;      // row tile; -1: none left
-    int n;          // column tile
+// A workgroup's share of the tiles.  Workgroups go to the eight XCDs in turn:
+// each XCD gets one run of the tiles, ordered so that the 32 it has at a time
+// are 4 row tiles x 8 column tiles, whose operands its L2 shares.
+struct TileShare {
+    int64_t row_tiles, first;   // first: this workgroup's; the next ones follow `step` apart
+    int32_t count, step, n_tiles;
+
+    __device__ TileShare(int64_t row_tiles_, int n_tiles_) {
+        row_tiles = row_tiles_;
+        n_tiles = n_tiles_;
+        const int64_t all = row_tiles * n_tiles, per = all / 8, extra = all % 8;
+        const int xcd = (int)(blockIdx.x % 8u), slot = (int)(blockIdx.x / 8u);
+        step = (int)(gridDim.x / 8u);
+        const int64_t run = per + (xcd < extra);
+        first = xcd * per + (xcd < extra ? xcd : extra) + slot;
+        count = slot < run ? (int)((run - slot + step - 1) / step) : 0;
+    }
+
+    // row tile and column tile of the workgroup's i-th tile
+    __device__ void place(int i, int64_t* m, int* n) const {
+        const int64_t at = first + (int64_t)i * step, wide = 4 * (int64_t)n_tiles;
+        const int64_t band = at / wide;
+        const int in = (int)(at - band * wide);
+        const int64_t left = row_tiles - band * 4;
+        const int rows = (int)(left < 4 ? left : 4);
+        *m = band * 4 + in % rows;
+        *n = in / rows;
+    }
 };
 
-__device__ inline TilePlace place_tile(int64_t row_tiles, int n_tiles) {
-    const int64_t all = row_tiles * n_tiles;
-    const int xcd = (int)(blockIdx.x % 8u);
-    const int64_t slot = blockIdx.x / 8u, per = all / 8, extra = all % 8;
-    if (slot >= per + (xcd < extra)) return {-1, 0};
-    const int64_t at = xcd * per + (xcd < extra ? xcd : extra) + slot;
-    const int64_t band = at / (4 * n_tiles), in = at - band * 4 * n_tiles;
-    const int64_t left = row_tiles - band * 4;
-    const int64_t rows = left < 4 ? left : 4;
-    return {band * 4 + in % rows, (int)(in / rows)};
+// out[k] of lane group g (16 lanes each) = c[g] of lane group k.
+__device__ inline void transpose4(uint32_t* c) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const u32x2 p = __builtin_amdgcn_permlane32_swap(c[k], c[k + 2], false, false);
+        c[k] = p[0];
+        c[k + 2] = p[1];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+        const u32x2 p = __builtin_amdgcn_permlane16_swap(c[k], c[k + 1], false, false);
+        c[k] = p[0];
+        c[k + 1] = p[1];
+    }
 }
 
 template <bool GATE>
 __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs a) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[5 * kOperandBytes];
     if (blockIdx.x == 0) check_groups(a);
-    const TilePlace place =
-        place_tile(count_tiles(a.group_offset, a.G, a.M, kBigRows), a.n_tiles);
-    if (place.m < 0) return;
-    const int nt = place.n;
-    const RowTile tile = find_tile(a.group_offset, a.G, a.M, place.m, kBigRows);
-    if (tile.g < 0) return;
+    const TileShare share(count_tiles(a.group_offset, a.G, a.M, kBigRows), a.n_tiles);
+    if (share.count == 0) return;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     // wavefronts 2 wm and 2 wm + 1 share rows: where a tile has few rows, those
     // without any idle on every SIMD alike
     const int wn = wave % 2, wm = wave / 2;
     const int nb = a.K / kScaleBlock;
     const int F = a.N / 2;
+    const int scale_rows = (a.N + 127) / 128;
 
-    // What this lane copies: rows wave * 32 + i * 8 + lane / 8 of both operands.
-    // Sixteen-byte chunk c of row r sits at chunk c ^ (r / 2 % 8) of its 128
-    // bytes, so that 16 rows' reads of one chunk meet all 64 banks once.  Rows
-    // behind the last repeat it; their results are not stored.
-    const int n0 = GATE ? (wave < 4 ? 0 : F - 128) + nt * 128 : nt * kBigRows;
-    const uint8_t* const wbase = a.w + ((int64_t)tile.g * a.N + n0) * a.K;
-    const uint8_t* const xbase = a.rows + tile.first * a.row_bytes;
-    // 256 rows of at most 2^20 + 2^15 bytes each: offsets stay below 2^31
-    const __amdgpu_buffer_rsrc_t wbuf = buffer_rsrc(const_cast<uint8_t*>(wbase), kBigRows * a.K);
-    const __amdgpu_buffer_rsrc_t xbuf =
-        buffer_rsrc(const_cast<uint8_t*>(xbase), tile.count * a.row_bytes);
-    uint32_t ow[4], ox[4];
+    // Where the copies stand: block `fb` of tile `ft`.  This lane copies rows
+    // wave * 32 + i * 8 + lane / 8 of both operands.  Sixteen-byte chunk c of row
+    // q sits at chunk c ^ (q / 2 % 8) of its 128 bytes, so that 16 rows' reads of
+    // one chunk meet all 64 banks once.  The buffers end with the last weight row
+    // and the tile's last row: what lies behind reads as zero, and its results
+    // are not stored.  For the gate, a wavefront's 128 weight rows are 64 gates
+    // and the 64 ups of the same outputs.
+    int ft = 0, fb = 0;
+    __amdgpu_buffer_rsrc_t wbuf, xbuf;
+    const float* psw[GATE ? 2 : 1];
+    const auto aim = [&](int t) {
+        int64_t m;
+        int nt;
+        share.place(t, &m, &nt);
+        const RowTile tile = find_tile(a.group_offset, a.G, a.M, m, kBigRows);
+        const int count = tile.g < 0 ? 1 : tile.count;
+        const int64_t first = tile.g < 0 ? 0 : tile.first;
+        const int e = tile.g < 0 ? 0 : tile.g;
+        // this wavefront's 32 weight rows; offsets stay below 32 (2^20 + 2^15)
+        const int n0 = GATE ? wave % 4 / 2 * F + nt * 128 + wave / 4 * 64 + wave % 2 * 32
+                            : nt * kBigRows + wave * 32;
+        const int base = n0 < a.N ? n0 : a.N - 1;
+        const int rows = a.N - base < 32 ? a.N - base : 32;
+        wbuf = buffer_rsrc(const_cast<uint8_t*>(a.w) + ((int64_t)e * a.N + base) * a.K, rows * a.K);
+        // and the tile's rows: below 256 (2^20 + 2^15)
+        xbuf = buffer_rsrc(const_cast<uint8_t*>(a.rows) + first * a.row_bytes,
+                           count * a.row_bytes);
+        if constexpr (GATE) {
+            psw[0] = a.w_scale + ((int64_t)e * scale_rows + nt) * nb;
+            psw[GATE] = psw[0] + (int64_t)(F / 128) * nb;
+        } else {
+            const int sr = nt * 2 + wn < scale_rows ? nt * 2 + wn : scale_rows - 1;
+            psw[0] = a.w_scale + ((int64_t)e * scale_rows + sr) * nb;
+        }
+    };
+    // lane's offsets for i = 0; chunk and chunk ^ 4 alternate with i
+    uint32_t ow = (uint32_t)(lane / 8) * a.K + ((lane % 8) ^ (lane / 16)) * 16;
+    uint32_t ox = (uint32_t)(wave * 32 + lane / 8) * a.row_bytes + ((lane % 8) ^ (lane / 16)) * 16;
+    uint32_t osx = (uint32_t)(wm * 64 + lane % 16) * a.row_bytes + a.K;
+    // behind the last tile the copies repeat its last block
+    const auto advance = [&]() {
+        if (++fb < nb) return;
+        if (ft + 1 < share.count) {
+            fb = 0;
+            aim(++ft);
+        } else {
+            fb = nb - 1;
+        }
+    };
+    const auto fetch_w = [&](uint32_t at, int i) {
+        to_lds(wbuf, (ow ^ (i % 2 * 64)) + (uint32_t)(i * 8) * a.K, fb * kScaleBlock,
+               s_mem + at + wave * 4096 + i * 1024);
+    };
+    const auto fetch_x = [&](uint32_t at, int i) {
+        to_lds(xbuf, (ox ^ (i % 2 * 64)) + (uint32_t)(i * 8) * a.row_bytes, fb * kScaleBlock,
+               s_mem + at + wave * 4096 + i * 1024);
+    };
+    // scales of block fb: this lane's rows, this wavefront's weight rows
+    float sx[4], sw[GATE ? 2 : 1];
+    const auto scales = [&]() {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sx[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                xbuf, osx + (uint32_t)(j * 16) * a.row_bytes, 4 * fb, 0));
+        sw[0] = psw[0][fb];
+        if constexpr (GATE) sw[GATE] = psw[GATE][fb];
+    };
+    const int at0 = lane % 16 * 128 + ((lane / 16 ^ (lane % 16 / 2)) * 16), at1 = at0 ^ 64;
+    const auto wtile = [&](uint32_t at, int i) {
+        const uint8_t* l = s_mem + at + wn * 16384 + i * 2048;
+        return join(load16(l + at0), load16(l + at1));
+    };
+    const auto xtile = [&](uint32_t at, int j) {
+        const uint8_t* l = s_mem + at + wm * 8192 + j * 2048;
+        return join(load16(l + at0), load16(l + at1));
+    };
+
+    // places of this, the next and the over-next block
+    uint32_t w_at[3] = {0, kOperandBytes, 2 * kOperandBytes};
+    uint32_t x_at[2] = {kRowsAt, kRowsAt + kOperandBytes};
+    constexpr int kS = GATE ? 8 : 4;       // scale products: gates' rows, then ups'
+    float s[kS], sp[2] = {0.0f, 0.0f};
+    const auto products = [&]() {
+#pragma unroll
+        for (int k = 0; k < kS; ++k) s[k] = sx[k % 4] * sw[k / 4];
+    };
+    aim(0);
+    scales();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = wave * 32 + i * 8 + lane / 8;
-        const int c = (lane % 8) ^ (r / 2 % 8);
-        const int n = n0 + r < a.N ? r : a.N - 1 - n0;
-        ow[i] = (uint32_t)n * (uint32_t)a.K + c * 16;
-        ox[i] = (uint32_t)(r < tile.count ? r : tile.count - 1) * (uint32_t)a.row_bytes + c * 16;
+        fetch_w(w_at[0], i);
+        fetch_x(x_at[0], i);
     }
-    // one of the four parts of this wavefront's copy of block b
-    const auto fetch_w = [&](int b, int i) {
-        to_lds(wbuf, ow[i], b * kScaleBlock,
-               s_mem + b % 3 * kOperandBytes + wave * 4096 + i * 1024);
-    };
-    const auto fetch_x = [&](int b, int i) {
-        to_lds(xbuf, ox[i], b * kScaleBlock,
-               s_mem + kRowsAt + (b & 1) * kOperandBytes + wave * 4096 + i * 1024);
-    };
+    meet<0, 0>();
+    products();
+    advance();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        fetch_w(w_at[1], i);
+        fetch_x(x_at[1], i);
+    }
 
-    f32x4 acc[8][4];
+    f32x4 acc[8][4], t[4];
+    i32x8 w[3], x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[j] = xtile(x_at[0], j);
+        t[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    w[0] = wtile(w_at[0], 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int r = lane % 16, g = lane / 16;
 
-    // Copies are spread over the work, one an i, in this order: in block b's
-    // i = 0, 1 the second half of rows b + 1, in i = 2 .. 5 weights b + 2, then,
-    // behind the meeting, scales b + 2 and in i = 6, 7 the first half of rows
-    // b + 2.  The meeting waits for all but weights b + 2.
+    // One block of K: 32 MFMAs q = 4 i + j, each followed by the scaled sum of
+    // the one two before it, so that neither unit waits for the other.  Weight
+    // tiles are read two ahead.  Two meetings: at i = 1 every wavefront has its
+    // rows in registers, and their place takes rows of the block two ahead; at
+    // i = 6 every wavefront has read its weights and the next block has arrived
+    // (all but the eight copies of the one after it), whose first reads follow
+    // under the MFMAs left.  A wavefront without rows copies and meets only.
+    const auto block = [&](auto busy) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        fetch_w(0, i);
-        fetch_x(0, i);
-    }
-    if (wm * 64 >= tile.count) {
-        // no rows of its own: this wavefront only copies
-        if (nb > 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) fetch_w(1, i);
-            fetch_x(1, 0);
-            fetch_x(1, 1);
-            meet<6>();
-        } else {
-            meet<0>();
-        }
-        for (int b = 0; b < nb - 1; ++b) {
-            fetch_x(b + 1, 2);
-            fetch_x(b + 1, 3);
-            if (b + 2 < nb) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) fetch_w(b + 2, i);
-                meet<4>();
-                fetch_x(b + 2, 0);
-                fetch_x(b + 2, 1);
-            } else {
-                meet<0>();
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (busy.value) {
+                if (i == 0) w[1] = wtile(w_at[0], 1);
+                // the two reads of weight tile 2 may be under way, not the rows'
+                if (i == 1) meet<63, 2>();
+                if (i < 6) w[(i + 2) % 3] = wtile(w_at[0], i + 2);
             }
-        }
-    } else {
-        // scales: this lane's four rows, this wavefront's block of weight rows
-        uint32_t osx[4];
+            if constexpr (!busy.value)
+                if (i == 1) meet<63, 0>();
+            if (i < 4) fetch_w(w_at[2], i);
+            if (i >= 2 && i < 6) fetch_x(x_at[0], i - 2);
+            if (i == 6) meet<8, 0>();
+            if (i == 7) w[0] = wtile(w_at[1], 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = wm * 64 + j * 16 + r;
-            osx[j] = (uint32_t)(m < tile.count ? m : tile.count - 1) * (uint32_t)a.row_bytes + a.K;
-        }
-        const int scale_rows = (a.N + 127) / 128;
-        int sr = GATE ? (wn ? F / 128 : 0) + nt : nt * 2 + wn;
-        sr = sr < scale_rows ? sr : scale_rows - 1;
-        const float* psw = a.w_scale + ((int64_t)tile.g * scale_rows + sr) * nb;
-        float sx[4], sw, s[4], sn[4], sp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const auto scales = [&](int b) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                sx[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(xbuf, osx[j], 4 * b, 0));
-            sw = psw[b];
-        };
-        const int at0 = r * 128 + ((g ^ (r / 2)) * 16), at1 = at0 ^ 64;
-        const auto wtile = [&](int b, int i) {
-            const uint8_t* l = s_mem + b % 3 * kOperandBytes + wn * 16384 + i * 2048;
-            return join(load16(l + at0), load16(l + at1));
-        };
-        const auto xtile = [&](int b, int j) {
-            const uint8_t* l =
-                s_mem + kRowsAt + (b & 1) * kOperandBytes + wm * 8192 + j * 2048;
-            return join(load16(l + at0), load16(l + at1));
-        };
-
-        scales(0);
-        if (nb > 1) {
-            const float sx0[4] = {sx[0], sx[1], sx[2], sx[3]}, sw0 = sw;
-            scales(1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) fetch_w(1, i);
-            fetch_x(1, 0);
-            fetch_x(1, 1);
-            meet<11>();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = sx0[j] * sw0;
-        } else {
-            meet<0>();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = sx[j] * sw;
-        }
-        // One block of K: 32 MFMAs q = 4 i + j, each followed by the scaled sum
-        // of the one two before it, so that neither unit waits for the other.
-        // Weight tiles are read two ahead.  When the last of this block's LDS
-        // reads is back (i = 6), the wavefronts meet: block b + 1 has arrived
-        // for all, and block b's places are free; the MFMAs left cover the
-        // meeting and the first reads of block b + 1.
-        i32x8 w[3], x[4];
-        f32x4 t[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] = xtile(0, j);
-            t[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        w[0] = wtile(0, 0);
-        // left: blocks after this one, 2 for two or more
-        const auto block = [&](int b, auto left) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i == 0) w[1] = wtile(b, 1);
-                if (i < 6) w[(i + 2) % 3] = wtile(b, i + 2);
-                if constexpr (left.value > 0) {
-                    if (i < 2) fetch_x(b + 1, i + 2);
-                    if constexpr (left.value > 1)
-                        if (i >= 2 && i < 6) fetch_w(b + 2, i - 2);
-                    if (i == 6) {
-                        meet<(left.value > 1 ? 4 : 0)>();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) sn[j] = sx[j] * sw;
-                        if constexpr (left.value > 1) scales(b + 2);
-                    }
-                    if constexpr (left.value > 1)
-                        if (i >= 6) fetch_x(b + 2, i - 6);
-                    if (i == 7) w[0] = wtile(b + 1, 0);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (busy.value) {
                     const int q = 4 * i + j, p = (q + 30) % 32;
                     __builtin_amdgcn_sched_barrier(0);
                     t[q % 4] = mfma16(w[i % 3], x[j]);
-                    acc[p / 4][p % 4] =
-                        fma4(t[p % 4], q < 2 ? sp[p % 4] : s[p % 4], acc[p / 4][p % 4]);
-                    if constexpr (left.value > 0)
-                        if (i == 7) x[j] = xtile(b + 1, j);
+                    acc[p / 4][p % 4] = fma4(
+                        t[p % 4], q < 2 ? sp[q] : s[(GATE ? p / 16 * 4 : 0) + p % 4], acc[p / 4][p % 4]);
                 }
+                if (i == 7) x[j] = xtile(x_at[1], j);
             }
-            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (busy.value) __builtin_amdgcn_sched_barrier(0);
+        sp[0] = s[kS - 2];
+        sp[1] = s[kS - 1];
+        products();
+        const uint32_t w0 = w_at[0], x0 = x_at[0];
+        w_at[0] = w_at[1];
+        w_at[1] = w_at[2];
+        w_at[2] = w0;
+        x_at[0] = x_at[1];
+        x_at[1] = x0;
+    };
+
+    for (int ti = 0; ti < share.count; ++ti) {
+        int64_t m;
+        int nt;
+        share.place(ti, &m, &nt);
+        const RowTile tile = find_tile(a.group_offset, a.G, a.M, m, kBigRows);
+        const int count = tile.g < 0 ? 0 : tile.count;
+        const bool busy = wm * 64 < count;
+        for (int b = 0; b < nb; ++b) {
+            // the offsets of each i are not worth registers of their own
+            asm volatile("" : "+v"(ow), "+v"(ox), "+v"(osx));
+            scales();    // of the next block, before the copies that the meeting leaves
+            advance();
+            if (busy)
+                block(std::true_type{});
+            else
+                block(std::false_type{});
+        }
+        if (busy) {
+#pragma unroll
+            for (int p = 30; p < 32; ++p)
+                acc[p / 4][p % 4] = fma4(t[p % 4], sp[p - 30], acc[p / 4][p % 4]);
+        }
+        // (opaque: addresses made from them are not worth registers in the loop)
+        int r = lane % 16, g = lane / 16;
+        asm volatile("" : "+v"(r), "+v"(g));
+        if constexpr (!GATE) {
+            // A lane has columns 4 g .. 4 g + 3 of each 16: two neighbouring
+            // tiles' halves change hands, so that it has 8 of one of them.
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                sp[j] = s[j];
-                s[j] = sn[j];
-            }
-        };
-        for (int b = 0; b < nb - 2; ++b) block(b, std::integral_constant<int, 2>{});
-        if (nb > 1) block(nb - 2, std::integral_constant<int, 1>{});
-        block(nb - 1, std::integral_constant<int, 0>{});
-#pragma unroll
-        for (int p = 30; p < 32; ++p)
-            acc[p / 4][p % 4] = fma4(t[p % 4], sp[p % 4], acc[p / 4][p % 4]);
-    }
-
-    if constexpr (!GATE) {
-        // lane: columns 4 g .. 4 g + 3 of each 16, one row of each 16
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = wm * 64 + j * 16 + r;
-            if (m >= tile.count) continue;
-            uint8_t* row = a.out + (tile.first + m) * a.out_bytes;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = nt * kBigRows + wn * 128 + i * 16 + g * 4;
-                if (c < a.N)
-                    *reinterpret_cast<u32x2*>(row + 2 * c) =
-                        u32x2{bf16_pack(acc[i][j][0], acc[i][j][1]),
-                              bf16_pack(acc[i][j][2], acc[i][j][3])};
-            }
-        }
-    } else {
-        // The gates' wavefront hands the ups' the second half of its rows and
-        // takes the first half of the ups' rows: 16 KB each way a pair, in the
-        // lanes' own order.
-        __syncthreads();
-        f32x4* const mine = reinterpret_cast<f32x4*>(s_mem) + wave * 1024;
-        f32x4* const other = reinterpret_cast<f32x4*>(s_mem) + (wave ^ 1) * 1024;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mine[(i * 2 + j) * 64 + lane] = pick(wn, acc[i][j], acc[i][j + 2]);
-            }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float h[8][4];
-            float am = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const f32x4 got = other[(i * 2 + j) * 64 + lane];
-                const f32x4 own = pick(wn, acc[i][j + 2], acc[i][j]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    h[i][q] = silu_mul(wn ? got[q] : own[q], wn ? own[q] : got[q]);
-                    am = fmaxf(am, fabsf(h[i][q]));
-                }
-            }
-            am = fmaxf(am, __shfl_xor(am, 16));
-            am = fmaxf(am, __shfl_xor(am, 32));
-            am = fmaxf(am, kAmaxMin);
-            const int m = wm * 64 + (wn * 2 + j) * 16 + r;
-            if (m < tile.count) {
-                uint8_t* row = a.out + (tile.first + m) * a.out_bytes;
-                const float inv = kFp8Max / am;
+                const int row = wm * 64 + j * 16 + r;
+                uint8_t* out = a.out + (tile.first + row) * a.out_bytes;
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
-                    const float p[8] = {h[i][0], h[i][1], h[i][2], h[i][3],
-                                        h[i + 1][0], h[i + 1][1], h[i + 1][2], h[i + 1][3]};
-                    const u32x2 code = fp8_pack8(p, inv);
-                    *reinterpret_cast<uint32_t*>(row + nt * 128 + i * 16 + g * 4) = code.x;
-                    *reinterpret_cast<uint32_t*>(row + nt * 128 + i * 16 + 16 + g * 4) = code.y;
+                    const u32x2 lo = __builtin_amdgcn_permlane16_swap(
+                        bf16_pack(acc[i][j][0], acc[i][j][1]),
+                        bf16_pack(acc[i + 1][j][0], acc[i + 1][j][1]), false, false);
+                    const u32x2 hi = __builtin_amdgcn_permlane16_swap(
+                        bf16_pack(acc[i][j][2], acc[i][j][3]),
+                        bf16_pack(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
+                    const int c = nt * kBigRows + wn * 128 + (i + g % 2) * 16 + g / 2 * 8;
+                    if (row < count && c < a.N)
+                        *reinterpret_cast<u32x4*>(out + 2 * c) = u32x4{lo[0], hi[0], lo[1], hi[1]};
                 }
-                if (g == 0) *reinterpret_cast<float*>(row + F + 4 * nt) = am / kFp8Max;
-                if (nt == F / 128 - 1)
-                    for (int o = F + F / 32 + 4 * g; o < a.out_bytes; o += 16)
-                        *reinterpret_cast<uint32_t*>(row + o) = 0u;
+            }
+        } else {
+            // silu(gate) * up in place of the gates; the block's maximum is that
+            // of two wavefronts, through the place of the block just used (free
+            // until the next block's copies)
+            float* const s_max = reinterpret_cast<float*>(s_mem + w_at[2]);
+            float am[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                am[j] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        acc[i][j][q] = silu_mul(acc[i][j][q], acc[i + 4][j][q]);
+                        am[j] = fmaxf(am[j], fabsf(acc[i][j][q]));
+                    }
+                am[j] = fmaxf(am[j], __shfl_xor(am[j], 16));
+                am[j] = fmaxf(am[j], __shfl_xor(am[j], 32));
+                if (g == 0) s_max[wave * 64 + j * 16 + r] = am[j];
+            }
+            meet<63, 0>();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                am[j] = fmaxf(fmaxf(am[j], s_max[(wave ^ 1) * 64 + j * 16 + r]), kAmaxMin);
+            meet<63, 0>();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = wm * 64 + j * 16 + r;
+                uint8_t* out = a.out + (tile.first + row) * a.out_bytes;
+                const float inv = kFp8Max / am[j];
+                uint32_t c[4];
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const float h[8] = {acc[i][j][0],     acc[i][j][1],     acc[i][j][2],
+                                        acc[i][j][3],     acc[i + 1][j][0], acc[i + 1][j][1],
+                                        acc[i + 1][j][2], acc[i + 1][j][3]};
+                    const u32x2 code = fp8_pack8(h, inv);
+                    c[i] = code[0];
+                    c[i + 1] = code[1];
+                }
+                transpose4(c);   // this lane: outputs 16 g .. 16 g + 15 of the wavefront's 64
+                if (row < count) {
+                    *reinterpret_cast<u32x4*>(out + nt * 128 + wn * 64 + g * 16) =
+                        u32x4{c[0], c[1], c[2], c[3]};
+                    if (wn == 0 && g == 0)
+                        *reinterpret_cast<float*>(out + F + 4 * nt) = am[j] / kFp8Max;
+                    if (wn == 1 && nt == F / 128 - 1)
+                        for (int o = F + F / 32 + 4 * g; o < a.out_bytes; o += 16)
+                            *reinterpret_cast<uint32_t*>(out + o) = 0u;
+                }
             }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            t[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
     }
+    wait_vm();   // no copy may reach the LDS after the workgroup's end
 }
 
 // A tile's 256 rows stay within 32-bit offsets.
@@ -612,22 +655,24 @@ int expert_args(ExpertArgs& a, int32_t G, int64_t M, int32_t N, int32_t K, const
     return EP_OK;
 }
 
-// Workgroups of a launch: column tiles x the row tiles that there can be,
-// rounded up to a multiple of `step`.
-int grid_of(const ExpertArgs& a, int bm, int step, unsigned* blocks) {
-    const int64_t n = ceil_div(max_tiles(a.M, a.G, bm) * a.n_tiles, step) * step;
+// Workgroups of a launch: one for each column tile of the row tiles that there
+// can be, or, `most` > 0, that many at most, a multiple of the eight XCDs, which
+// share the tiles out.
+int grid_of(const ExpertArgs& a, int bm, int most, unsigned* blocks) {
+    int64_t n = max_tiles(a.M, a.G, bm) * a.n_tiles;
     if (n >= ((int64_t)1 << 31)) {
         record_error("expert product: more than 2^31 tiles");
         return EP_ERR_INVALID_ARG;
     }
+    if (most > 0) n = n < most ? ceil_div(n, 8) * 8 : most;
     *blocks = (unsigned)n;
     return EP_OK;
 }
 
-#define EP_LAUNCH_TILES(KERNEL, BM, THREADS, STEP)                                            \
+#define EP_LAUNCH_TILES(KERNEL, BM, THREADS, MOST)                                            \
     do {                                                                                   \
         unsigned blocks = 0;                                                               \
-        const int v_ = grid_of(a, BM, STEP, &blocks);                                      \
+        const int v_ = grid_of(a, BM, MOST, &blocks);                                      \
         if (v_ != EP_OK) return v_;                                                        \
         clear_hip_error();                                                                 \
         hipLaunchKernelGGL((KERNEL), dim3(blocks), dim3(THREADS), 0, stream, a);           \
@@ -650,11 +695,11 @@ extern "C" int ep_expert_product(int32_t G, int64_t M, int32_t N, int32_t K, con
     const int64_t per = ceil_div(M, G);   // rows a group, were they even
     if (per > 64) {
         a.n_tiles = (int32_t)ceil_div(N, kBigRows);
-        EP_LAUNCH_TILES(product_big_kernel<false>, kBigRows, kBigThreads, 8);
+        EP_LAUNCH_TILES(product_big_kernel<false>, kBigRows, kBigThreads, kBigGrid);
     }
-    if (per <= 16) EP_LAUNCH_TILES(product_small_kernel<1>, 16, 256, 1);
-    if (per <= 32) EP_LAUNCH_TILES(product_small_kernel<2>, 32, 256, 1);
-    EP_LAUNCH_TILES(product_small_kernel<4>, 64, 256, 1);
+    if (per <= 16) EP_LAUNCH_TILES(product_small_kernel<1>, 16, 256, 0);
+    if (per <= 32) EP_LAUNCH_TILES(product_small_kernel<2>, 32, 256, 0);
+    EP_LAUNCH_TILES(product_small_kernel<4>, 64, 256, 0);
 }
 
 extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, const void* rows,
@@ -670,8 +715,8 @@ extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, con
     a.out_bytes = (int32_t)row_bytes(F, EP_FMT_FP8_E4M3_B128);
     a.n_tiles = F / kScaleBlock;
     const int64_t per = ceil_div(M, G);
-    if (per > 64) EP_LAUNCH_TILES(product_big_kernel<true>, kBigRows, kBigThreads, 8);
-    if (per <= 16) EP_LAUNCH_TILES(gate_up_small_kernel<1>, 16, 1024, 1);
-    if (per <= 32) EP_LAUNCH_TILES(gate_up_small_kernel<2>, 32, 1024, 1);
-    EP_LAUNCH_TILES(gate_up_small_kernel<4>, 64, 1024, 1);
+    if (per > 64) EP_LAUNCH_TILES(product_big_kernel<true>, kBigRows, kBigThreads, kBigGrid);
+    if (per <= 16) EP_LAUNCH_TILES(gate_up_small_kernel<1>, 16, 1024, 0);
+    if (per <= 32) EP_LAUNCH_TILES(gate_up_small_kernel<2>, 32, 1024, 0);
+    EP_LAUNCH_TILES(gate_up_small_kernel<4>, 64, 1024, 0);
 }
