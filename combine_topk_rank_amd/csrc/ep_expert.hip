@@ -114,64 +114,42 @@ __device__ inline f32x4 fma4(f32x4 v, float s, f32x4 acc) {
 
 __device__ inline i32x4 load16(const uint8_t* p) { return *reinterpret_cast<const i32x4*>(p); }
 
-// Adds blocks [b0, b1) of 16 weight rows times MT x 16 rows to acc.  wrow: this
-// lane's weight row; xrow[j]: its rows of the second operand; both in bounds.
-template <int MT>
-__device__ inline void stream_blocks(const uint8_t* wrow, const float* sw,
-                                     const uint8_t* const* xrow, int K, int b0, int b1,
-                                     f32x4* acc) {
-    const int g = lane_id() / 16 * 16;
-    for (int b = b0; b < b1; ++b) {
-        const int k = b * kScaleBlock + g;
-        const i32x8 w = join(load16(wrow + k), load16(wrow + k + 64));
-        const float s = sw[b];
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            const i32x8 x = join(load16(xrow[j] + k), load16(xrow[j] + k + 64));
-            const float sx = reinterpret_cast<const float*>(xrow[j] + K)[b];
-            acc[j] = fma4(mfma16(w, x), s * sx, acc[j]);
-        }
-    }
-}
-
 // Few rows a group: the weights are read once, straight from memory to
-// registers.  A workgroup has 16 weight rows and MT x 16 rows; its four
-// wavefronts split K and join in LDS in their order.
-template <int MT>
+// registers.  A workgroup has 16 weight rows and 16 rows; its four wavefronts
+// split K and join in LDS in their order.  Bound by memory: 5.2 TB/s for one
+// row at each of 8 experts, N = 7168, K = 1792 (20 us); enough workgroups are
+// resident that loads two or three blocks ahead only cost occupancy (22-25 us).
 __global__ __launch_bounds__(256) void product_small_kernel(ExpertArgs a) {
-    __shared__ f32x4 s_acc[4][MT][kWave];
+    __shared__ f32x4 s_acc[4][kWave];
     if (blockIdx.x == 0) check_groups(a);
     const int nt = (int)(blockIdx.x % (unsigned)a.n_tiles);
-    const RowTile tile =
-        find_tile(a.group_offset, a.G, a.M, blockIdx.x / (unsigned)a.n_tiles, 16 * MT);
+    const RowTile tile = find_tile(a.group_offset, a.G, a.M, blockIdx.x / (unsigned)a.n_tiles, 16);
     if (tile.g < 0) return;
     const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
     const int n0 = nt * 16, nb = a.K / kScaleBlock;
     // rows behind the last weight row or the tile's last row repeat the last
     // one: their results are not stored
     const int n = n0 + lane % 16 < a.N ? n0 + lane % 16 : a.N - 1;
+    const int m = lane % 16 < tile.count ? lane % 16 : tile.count - 1;
     const uint8_t* wrow = a.w + ((int64_t)tile.g * a.N + n) * a.K;
+    const uint8_t* xrow = a.rows + (tile.first + m) * a.row_bytes;
     const float* sw = a.w_scale + ((int64_t)tile.g * ((a.N + 127) / 128) + n0 / 128) * nb;
-    const uint8_t* xrow[MT];
-    f32x4 acc[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const int m = j * 16 + lane % 16;
-        xrow[j] = a.rows + (tile.first + (m < tile.count ? m : tile.count - 1)) * a.row_bytes;
-        acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int g = lane / 16 * 16, b1 = nb * (wave + 1) / 4;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = nb * wave / 4; b < b1; ++b) {
+        const int k = b * kScaleBlock + g;
+        const i32x8 w = join(load16(wrow + k), load16(wrow + k + 64));
+        const i32x8 x = join(load16(xrow + k), load16(xrow + k + 64));
+        acc = fma4(mfma16(w, x), sw[b] * reinterpret_cast<const float*>(xrow + a.K)[b], acc);
     }
-    stream_blocks<MT>(wrow, sw, xrow, a.K, nb * wave / 4, nb * (wave + 1) / 4, acc);
-#pragma unroll
-    for (int j = 0; j < MT; ++j) s_acc[wave][j][lane] = acc[j];
+    s_acc[wave][lane] = acc;
     __syncthreads();
-    for (int j = wave; j < MT; j += 4) {
-        const f32x4 v =
-            ((s_acc[0][j][lane] + s_acc[1][j][lane]) + s_acc[2][j][lane]) + s_acc[3][j][lane];
-        const int m = j * 16 + lane % 16, c = n0 + lane / 16 * 4;
-        if (m < tile.count && c < a.N)   // N is a multiple of 8: all four columns or none
-            *reinterpret_cast<u32x2*>(a.out + (tile.first + m) * a.out_bytes + 2 * c) =
-                u32x2{bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3])};
-    }
+    if (wave != 0) return;
+    const f32x4 v = ((s_acc[0][lane] + s_acc[1][lane]) + s_acc[2][lane]) + s_acc[3][lane];
+    const int c = n0 + lane / 16 * 4;
+    if (lane % 16 < tile.count && c < a.N)   // N is a multiple of 8: all four columns or none
+        *reinterpret_cast<u32x2*>(a.out + (tile.first + m) * a.out_bytes + 2 * c) =
+            u32x2{bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3])};
 }
 
 __device__ inline float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
@@ -191,43 +169,108 @@ __device__ inline void store_block(const ExpertArgs& a, int64_t m, int fb, const
 }
 
 // Few rows a group, with the gate: a workgroup has the 128 gates and 128 ups
-// of one output block and MT x 16 rows; wavefront w has 16 of those weight
-// rows over all of K.
-template <int MT>
+// of one output block and 16 rows; wavefront w has 16 of those weight rows over
+// all of K.  Weights go from memory to registers, four blocks (8 KB a wavefront)
+// under way; the 16 wavefronts share the rows through LDS, sixteen blocks at a
+// time and the next sixteen under way, since a CU takes no more than about 25
+// GB/s in all (reading the rows once a wavefront: 118 against 73 us for 4 rows
+// against one at each of 8 experts, 7168 x 1792).
+constexpr int kSlab = 16;                              // blocks of K of the rows in LDS
+constexpr int kSlabPitch = kSlab * kScaleBlock + 16;   // 16 rows' reads meet all banks once
+
 __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
     constexpr int kPitch = 2 * kScaleBlock + 4;
-    __shared__ float s_y[16 * MT][kPitch];
+    constexpr int kAhead = 4;
+    __shared__ __attribute__((aligned(16))) uint8_t s_x[2][16][kSlabPitch];
+    __shared__ float s_sx[2][16][kSlab];
+    static_assert(sizeof(float) * 16 * kPitch <= sizeof s_x, "the outputs reuse the rows' LDS");
+    float(*const s_y)[kPitch] = reinterpret_cast<float(*)[kPitch]>(s_x);
     if (blockIdx.x == 0) check_groups(a);
     const int fb = (int)(blockIdx.x % (unsigned)a.n_tiles);
-    const RowTile tile =
-        find_tile(a.group_offset, a.G, a.M, blockIdx.x / (unsigned)a.n_tiles, 16 * MT);
+    const RowTile tile = find_tile(a.group_offset, a.G, a.M, blockIdx.x / (unsigned)a.n_tiles, 16);
     if (tile.g < 0) return;
-    const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
+    const int tid = (int)threadIdx.x, lane = lane_id(), wave = tid / kWave;
     const int F = a.N / 2, nb = a.K / kScaleBlock;
     const int n0 = (wave < 8 ? 0 : F) + fb * kScaleBlock + wave % 8 * 16;
-    const uint8_t* wrow = a.w + ((int64_t)tile.g * a.N + n0 + lane % 16) * a.K;
+    const uint8_t* wrow =
+        a.w + ((int64_t)tile.g * a.N + n0 + lane % 16) * a.K + lane / 16 * 16;
     const float* sw = a.w_scale + ((int64_t)tile.g * (a.N / 128) + n0 / 128) * nb;
-    const uint8_t* xrow[MT];
-    f32x4 acc[MT];
+
+    // this thread's part of a slab: 32 bytes of one row, and a scale of 256
+    // threads.  Rows behind the tile's last repeat it, blocks behind the last
+    // block too; neither is used.
+    const int sr = tid / 64, sc = tid % 64;
+    const uint8_t* xrow = a.rows + (tile.first + (sr < tile.count ? sr : tile.count - 1)) * a.row_bytes;
+    i32x4 part[2];
+    float part_scale;
+    const auto read_slab = [&](int b0) {
+        const int b = b0 + sc / 4 < nb ? b0 + sc / 4 : nb - 1;
+        part[0] = load16(xrow + b * kScaleBlock + sc % 4 * 32);
+        part[1] = load16(xrow + b * kScaleBlock + sc % 4 * 32 + 16);
+        part_scale = reinterpret_cast<const float*>(xrow + a.K)[b];
+    };
+    const auto write_slab = [&](int to) {
+        *reinterpret_cast<i32x4*>(&s_x[to][sr][sc * 32]) = part[0];
+        *reinterpret_cast<i32x4*>(&s_x[to][sr][sc * 32 + 16]) = part[1];
+        if (sc % 4 == 0) s_sx[to][sr][sc / 4] = part_scale;
+    };
+
+    i32x8 w[kAhead];
+    float s[kAhead];
+    const auto load = [&](int d, int b) {
+        b = b < nb ? b : nb - 1;
+        w[d] = join(load16(wrow + b * kScaleBlock), load16(wrow + b * kScaleBlock + 64));
+        s[d] = sw[b];
+    };
+    read_slab(0);
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const int m = j * 16 + lane % 16;
-        xrow[j] = a.rows + (tile.first + (m < tile.count ? m : tile.count - 1)) * a.row_bytes;
-        acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int d = 0; d < kAhead; ++d) load(d, d);
+    write_slab(0);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint8_t* lx = nullptr;
+    const float* lsx = nullptr;
+    const auto use = [&](int d, int c) {
+        const i32x8 x = join(load16(lx + c * kScaleBlock), load16(lx + c * kScaleBlock + 64));
+        acc = fma4(mfma16(w[d], x), s[d] * lsx[c], acc);
+    };
+    // four blocks a step, those of the next step read behind them; the last
+    // step reads none (no load hides behind a branch, or the compiler would wait
+    // for all that are under way)
+    const int last = (nb - 1) / kAhead * kAhead;
+    for (int b = 0; b < last; b += kAhead) {
+        const int c = b % kSlab, turn = b / kSlab % 2;
+        if (c == 0) {
+            __syncthreads();
+            lx = &s_x[turn][lane % 16][lane / 16 * 16];
+            lsx = s_sx[turn][lane % 16];
+            if (b + kSlab < nb) read_slab(b + kSlab);
+        }
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+            use(d, c + d);
+            load(d, b + kAhead + d);
+        }
+        if (c == kSlab - kAhead && b + kAhead < nb) write_slab(turn ^ 1);
     }
-    stream_blocks<MT>(wrow, sw, xrow, a.K, 0, nb, acc);
+    if (last % kSlab == 0) {
+        __syncthreads();
+        lx = &s_x[last / kSlab % 2][lane % 16][lane / 16 * 16];
+        lsx = s_sx[last / kSlab % 2][lane % 16];
+    }
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-        *reinterpret_cast<f32x4*>(&s_y[j * 16 + lane % 16][wave * 16 + lane / 16 * 4]) = acc[j];
+    for (int d = 0; d < kAhead; ++d)
+        if (last + d < nb) use(d, last % kSlab + d);
+    __syncthreads();
+    *reinterpret_cast<f32x4*>(&s_y[lane % 16][wave * 16 + lane / 16 * 4]) = acc;
     __syncthreads();
     // 16 lanes a row, eight outputs each
-    for (int m = (int)threadIdx.x / 16; m < 16 * MT; m += 64) {
-        const float* y = &s_y[m][lane % 16 * 8];
-        float h[8];
+    if (tid >= 256) return;
+    const int row = tid / 16;
+    const float* y = &s_y[row][lane % 16 * 8];
+    float h[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) h[q] = silu_mul(y[q], y[kScaleBlock + q]);
-        store_block(a, tile.first + m, fb, h, m < tile.count);
-    }
+    for (int q = 0; q < 8; ++q) h[q] = silu_mul(y[q], y[kScaleBlock + q]);
+    store_block(a, tile.first + row, fb, h, row < tile.count);
 }
 
 // ---- Many rows a group ----------------------------------------------------------
@@ -692,14 +735,16 @@ extern "C" int ep_expert_product(int32_t G, int64_t M, int32_t N, int32_t K, con
     if (M == 0) return EP_OK;
     a.out_bytes = 2 * N;
     a.n_tiles = (int32_t)ceil_div(N, 16);
-    const int64_t per = ceil_div(M, G);   // rows a group, were they even
-    if (per > 64) {
+    // Rows a group, were they even.  Big tiles against small, us, unequal counts:
+    // 24 experts, 2176 x 896: 15.5 : 15.0 at 8 rows a group, 17.0 : 20.7 at 16;
+    // 8 experts, 7168 x 1792: 29.3 : 29.6 and 30.2 : 40.6; fewer rows are the
+    // small tiles', more the big ones'.
+    const int64_t per = ceil_div(M, G);
+    if (per > 8) {
         a.n_tiles = (int32_t)ceil_div(N, kBigRows);
         EP_LAUNCH_TILES(product_big_kernel<false>, kBigRows, kBigThreads, kBigGrid);
     }
-    if (per <= 16) EP_LAUNCH_TILES(product_small_kernel<1>, 16, 256, 0);
-    if (per <= 32) EP_LAUNCH_TILES(product_small_kernel<2>, 32, 256, 0);
-    EP_LAUNCH_TILES(product_small_kernel<4>, 64, 256, 0);
+    EP_LAUNCH_TILES(product_small_kernel, 16, 256, 0);
 }
 
 extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, const void* rows,
@@ -714,9 +759,9 @@ extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, con
     if (M == 0) return EP_OK;
     a.out_bytes = (int32_t)row_bytes(F, EP_FMT_FP8_E4M3_B128);
     a.n_tiles = F / kScaleBlock;
+    // As above, us: 24 experts, 2176 x 896: 39.8 : 37.2 at 16 rows a group, 43.5 :
+    // 62.7 at 24; 8 experts, 7168 x 1792: 96.8 : 79.9 and 102 : 82.0.
     const int64_t per = ceil_div(M, G);
-    if (per > 64) EP_LAUNCH_TILES(product_big_kernel<true>, kBigRows, kBigThreads, kBigGrid);
-    if (per <= 16) EP_LAUNCH_TILES(gate_up_small_kernel<1>, 16, 1024, 0);
-    if (per <= 32) EP_LAUNCH_TILES(gate_up_small_kernel<2>, 32, 1024, 0);
-    EP_LAUNCH_TILES(gate_up_small_kernel<4>, 64, 1024, 0);
+    if (per > 16) EP_LAUNCH_TILES(product_big_kernel<true>, kBigRows, kBigThreads, kBigGrid);
+    EP_LAUNCH_TILES(gate_up_small_kernel, 16, 1024, 0);
 }
