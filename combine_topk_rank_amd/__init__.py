@@ -350,11 +350,13 @@ def ep_combine_ll(s, y, topk_idx, topk_w, expert_slot, out, dev_status, stream=N
 # tensor: type, shape, contiguity and the current device.
 
 _U8 = _I32 = _F32 = _BF16 = _E4M3 = None   # torch types, set at the first call
+_device_now = _stream_of = None            # current device; its current stream's handle
 
 
 def _types() -> None:
     import torch
-    global _U8, _I32, _F32, _BF16, _E4M3
+    global _U8, _I32, _F32, _BF16, _E4M3, _device_now, _stream_of
+    _device_now, _stream_of = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
     _U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
     _E4M3 = torch.float8_e4m3fn
 
@@ -363,15 +365,16 @@ def _arg(name, t, dtype, shape_, device):
     """Address of tensor t after its checks; None for None."""
     if t is None:
         return None
+    if (t.dtype is dtype and t.shape == shape_ and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
     if t.shape != shape_:
         raise ValueError(f"{name} must have shape {tuple(shape_)}, has {tuple(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the current device ({device}), is on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _need(name, t):
@@ -382,16 +385,20 @@ def _need(name, t):
 
 def _call_device(stream):
     """Current device and the handle of the stream (default: its current one)."""
-    import torch
     if _U8 is None:
         _types()
-    device = torch.cuda.current_device()
+    device = _device_now()
     if stream is None:
-        return device, torch._C._cuda_getCurrentRawStream(device)
+        return device, _stream_of(device)
     if stream.device_index != device:
         raise ValueError(f"stream must be on the current device ({device}), is on "
                          f"{stream.device_index}")
     return device, stream.cuda_stream
+
+
+def _row8(H: int) -> int:
+    """ep_row_bytes of an 8-bit row"""
+    return -(-(H + H // 32) // 128) * 128
 
 
 def _workspace(t, device, needed):
@@ -415,7 +422,7 @@ def ep_rmsnorm(x, residual, weight, eps, residual_out=None, y=None, rows=None, r
         _arg("weight", _need("weight", weight), _F32, (H,), device), eps,
         _arg("residual_out", residual_out, _BF16, sh, device), _arg("y", y, _BF16, sh, device),
         None if rows is None else _arg("rows", rows, _U8,
-                                       (T, ep_row_bytes(H, EP_FMT_FP8_E4M3_B128)), device),
+                                       (T, _row8(H)), device),
         _arg("rstd", rstd, _F32, (T,), device), st_)
     _check(st, "ep_rmsnorm")
 
@@ -514,7 +521,7 @@ def _expert_args(rows, group_offset, w, w_scale, device):
     if w.dtype is not _U8 and w.dtype is not _E4M3:
         raise ValueError(f"w must be uint8 or float8_e4m3fn, is {w.dtype}")
     return (G, M, N, K,
-            _arg("rows", rows, _U8, (M, ep_row_bytes(K, EP_FMT_FP8_E4M3_B128)), device),
+            _arg("rows", rows, _U8, (M, _row8(K)), device),
             _arg("group_offset", _need("group_offset", group_offset), _I32, (G + 1,), device),
             _arg("w", w, w.dtype, (G, N, K), device),
             _arg("w_scale", _need("w_scale", w_scale), _F32, (G, -(-N // 128), K // 128), device))
@@ -538,7 +545,7 @@ def ep_expert_gate_up(rows, group_offset, w, w_scale, out_rows, dev_status, stre
     F = N // 2
     st = lib.ep_expert_gate_up(G, M, F, K, *inputs,
                                _arg("out_rows", _need("out_rows", out_rows), _U8,
-                                    (M, ep_row_bytes(F, EP_FMT_FP8_E4M3_B128)), device),
+                                    (M, _row8(F)), device),
                                _arg("dev_status", _need("dev_status", dev_status), _I32, (1,),
                                     device), st_)
     _check(st, "ep_expert_gate_up")

@@ -13,11 +13,13 @@
 //                   - (renormalised: sum_{j: e_j = e} topk_w_j S; else p_e S)
 // (the counts are constants of the gradient, as in the loss's definition).
 //
-// A token is a group of L lanes (16 for E <= 256, else a wavefront), each with
-// V consecutive logits in registers; one pass over the logits.  The choices
-// are k rounds of a maximum over the group; float maxima are exact, and the
-// lowest lane that holds the maximum, then its lowest register, is the lowest
-// expert that does.
+// A token is a group of L lanes (16 for E <= 256, else a wavefront), each with V
+// logits in registers, four neighbours of every 4 L; one pass over the logits.
+// The choices are k rounds of a maximum over the group (exact in float), then
+// of the lowest expert that has it.
+//
+// Bound: 16384 tokens of 256 experts are 16.8 MB of logits, 3.4 us at a copy's
+// rate; the k rounds cost about 90 instructions for four tokens each, 6 us.
 
 #include "ep_rows8.h"
 
@@ -38,42 +40,97 @@ struct GateArgs {
     int32_t T, E, k, renorm;
 };
 
+// Expert of register i of lane `sub` of a group of L lanes.
+template <int L>
+__device__ inline int expert_of(int sub, int i) {
+    return i / 4 * (4 * L) + sub * 4 + i % 4;
+}
+
 template <typename F>
-__device__ inline float load_logit(const void* p, int64_t i);
+struct Logits;
 template <>
-__device__ inline float load_logit<float>(const void* p, int64_t i) {
-    return reinterpret_cast<const float*>(p)[i];
-}
-template <>
-__device__ inline float load_logit<uint16_t>(const void* p, int64_t i) {
-    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
-}
-
-// The V logits of a lane from expert e0 on; -inf behind the last expert.
-template <typename F, int V>
-__device__ inline void load_logits(const void* p, int64_t base, int e0, int E, float* v) {
+struct Logits<float> {
+    __device__ static float one(const void* p, int64_t i) {
+        return reinterpret_cast<const float*>(p)[i];
+    }
+    __device__ static void four(const void* p, int64_t i, float* v) {
+        const f32x4 q = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        v[i] = e0 + i < E ? load_logit<F>(p, base + e0 + i) : -__builtin_inff();
+        for (int k = 0; k < 4; ++k) v[k] = q[k];
+    }
+    __device__ static void put(void* p, int64_t i, float v) { reinterpret_cast<float*>(p)[i] = v; }
+    __device__ static void put4(void* p, int64_t i, const float* v) {
+        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i) = f32x4{v[0], v[1], v[2], v[3]};
+    }
+};
+template <>
+struct Logits<uint16_t> {
+    __device__ static float one(const void* p, int64_t i) {
+        return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
+    }
+    __device__ static void four(const void* p, int64_t i, float* v) {
+        const u32x2 q = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(p) + i);
+        v[0] = bf16_lo(q[0]);
+        v[1] = bf16_hi(q[0]);
+        v[2] = bf16_lo(q[1]);
+        v[3] = bf16_hi(q[1]);
+    }
+    __device__ static void put(void* p, int64_t i, float v) {
+        reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)bf16_pack(v, 0.0f);
+    }
+    __device__ static void put4(void* p, int64_t i, const float* v) {
+        *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p) + i) =
+            u32x2{bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3])};
+    }
+};
+
+// A lane's logits of the token whose logits start at `base`; -inf behind the
+// last expert.  WIDE: four at a time (E % 4 == 0, four logits' alignment).
+template <typename F, int L, int V, bool WIDE>
+__device__ inline void load_logits(const void* p, int64_t base, int sub, int E, float* v) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const int e = expert_of<L>(sub, i);
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i + k] = -__builtin_inff();
+            if (e < E) Logits<F>::four(p, base + e, v + i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[i + k] = e + k < E ? Logits<F>::one(p, base + e + k) : -__builtin_inff();
+        }
+    }
 }
 
-template <typename F, int L, int V, bool STATS>
-__global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
-    extern __shared__ int32_t s_gate[];   // STATS: [E] counts, then [E] float sums
-    constexpr int kGroups = 256 / L;
-    const int sub = (int)threadIdx.x % L, e0 = sub * V;
-    const int group0 = lane_id() & ~(L - 1);            // first lane of this group
-    const uint64_t lanes = L == 64 ? ~0ull : ((1ull << (L & 63)) - 1);
+// Threads of a workgroup of a call with counts, which leaves one partial sum a
+// workgroup: as many wavefronts, up to 16, as have room for their sums in 32 KB
+// of LDS (joining them there in turn took 14 of 23 us at 4096 tokens of 256
+// experts).
+constexpr int gate_threads(int E) {
+    return E <= 512 ? 1024 : E <= 1024 ? 512 : E <= 2048 ? 256 : 128;
+}
+
+template <typename F, int L, int V, bool WIDE, bool STATS>
+__global__ __launch_bounds__(STATS ? gate_threads(L * V) : 256) void gate_kernel(GateArgs a) {
+    // STATS: [E, rounded up to 4] counts, then as many float sums a wavefront
+    extern __shared__ __attribute__((aligned(16))) int32_t s_gate[];
+    constexpr int kThreads = STATS ? gate_threads(L * V) : 256;
+    constexpr int kGroups = kThreads / L;
+    constexpr int kHold = L == 16 ? 2 : 1;     // lane j of a group holds choices j and j + L
+    const int sub = (int)threadIdx.x % L;
     float sum_p[V];
     int kept = 0;
     if constexpr (STATS) {
 #pragma unroll
         for (int i = 0; i < V; ++i) sum_p[i] = 0.0f;
-        for (int e = (int)threadIdx.x; e < a.E; e += 256) s_gate[e] = 0;
+        for (int e = (int)threadIdx.x; e < a.E; e += kThreads) s_gate[e] = 0;
         __syncthreads();
     }
     for (int64_t t = (int64_t)blockIdx.x * kGroups + (int)threadIdx.x / L; t < a.T;
          t += (int64_t)gridDim.x * kGroups) {
+        float v[V];
+        load_logits<F, L, V, WIDE>(a.logits, t * a.E, sub, a.E, v);   // under way with the mask
         if (a.mask && !a.mask[t]) {
             for (int j = sub; j < a.k; j += L) {
                 a.topk_idx[t * a.k + j] = -1;
@@ -82,8 +139,6 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
             if (a.lse && sub == 0) a.lse[t] = 0.0f;
             continue;
         }
-        float v[V], x[V];
-        load_logits<F, V>(a.logits, t * a.E, e0, a.E, v);
         float top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < V; ++i) top = fmaxf(top, v[i]);
@@ -91,26 +146,28 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
         // a row without a finite logit: every exponential is zero, not NaN
         const float shift = top == -__builtin_inff() ? 0.0f : top;
         float total = 0.0f;
+        {
+            float x[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            x[i] = expf(v[i] - shift);
-            total += x[i];
-        }
-        total = group_sum<L>(total);
-        if constexpr (STATS) {
-            const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+            for (int i = 0; i < V; ++i) {
+                x[i] = expf(v[i] - shift);
+                total += x[i];
+            }
+            total = group_sum<L>(total);
+            if constexpr (STATS) {
+                const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum_p[i] += x[i] * inv;
-            kept += sub == 0;
+                for (int i = 0; i < V; ++i) sum_p[i] = fmaf(x[i], inv, sum_p[i]);
+                kept += sub == 0;
+            }
         }
         if (a.lse && sub == 0) a.lse[t] = top + logf(total);
 
-        float chosen = 0.0f;                       // exponentials of the chosen
-        float my_w[L == 16 ? 2 : 1];               // lane j holds choices j and j + L
-        int my_e[L == 16 ? 2 : 1];
+        float my_v[kHold];
+        int my_e[kHold];
 #pragma unroll
-        for (int q = 0; q < (L == 16 ? 2 : 1); ++q) {
-            my_w[q] = 0.0f;
+        for (int q = 0; q < kHold; ++q) {
+            my_v[q] = -__builtin_inff();
             my_e[q] = -1;
         }
         for (int j = 0; j < a.k; ++j) {
@@ -119,56 +176,65 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
             for (int i = 0; i < V; ++i) m = fmaxf(m, v[i]);
             const float best = group_max<L>(m);
             if (!(best > -__builtin_inff())) break;   // only -inf and NaN are left
-            const uint64_t who = (__ballot(m == best) >> group0) & lanes;
-            const int winner = __builtin_ctzll(who);
             int at = V;
 #pragma unroll
             for (int i = V - 1; i >= 0; --i) at = v[i] == best ? i : at;
-            const int e = __shfl(e0 + at, group0 + winner);
-            if (sub == winner) {
+            const int mine = at < V ? expert_of<L>(sub, at) : 0x7FFFFFFF;
+            const int e = group_min<L>(mine);
+            at = mine == e ? at : V;
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = i == at ? -__builtin_inff() : v[i];
-            }
-            const float ex = expf(best - shift);
-            chosen += ex;
+            for (int i = 0; i < V; ++i) v[i] = i == at ? -__builtin_inff() : v[i];
 #pragma unroll
-            for (int q = 0; q < (L == 16 ? 2 : 1); ++q)
+            for (int q = 0; q < kHold; ++q)
                 if (j == sub + q * L) {
-                    my_w[q] = ex;
+                    my_v[q] = best;
                     my_e[q] = e;
                 }
-            if constexpr (STATS)
-                if (sub == 0) atomicAdd(&s_gate[e], 1);
         }
+        float my_w[kHold], chosen = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kHold; ++q) {
+            my_w[q] = expf(my_v[q] - shift);
+            chosen += my_w[q];
+        }
+        chosen = group_sum<L>(chosen);
         float scale = 1.0f / (a.renorm ? chosen : total);
         if (total != total) scale = total;   // a NaN logit makes every weight NaN
 #pragma unroll
-        for (int q = 0; q < (L == 16 ? 2 : 1); ++q) {
+        for (int q = 0; q < kHold; ++q) {
             const int j = sub + q * L;
             if (j < a.k) {
                 a.topk_idx[t * a.k + j] = my_e[q];
                 a.topk_w[t * a.k + j] = my_e[q] < 0 ? 0.0f : my_w[q] * scale;
+                if constexpr (STATS)
+                    if (my_e[q] >= 0) atomicAdd(&s_gate[my_e[q]], 1);
             }
         }
     }
     if constexpr (STATS) {
         // the groups of a wavefront, then the wavefronts, in a fixed order
-        float* s_sum = reinterpret_cast<float*>(s_gate + a.E);
+        const int E4 = (a.E + 3) / 4 * 4;
+        float* const s_sum = reinterpret_cast<float*>(s_gate + E4);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
             for (int o = L; o < 64; o *= 2) sum_p[i] += __shfl_xor(sum_p[i], o);
         }
-        for (int w = 0; w < 4; ++w) {
-            if ((int)threadIdx.x / kWave == w && lane_id() < L) {
+        if (lane_id() < L) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e0 + i < a.E) s_sum[e0 + i] = (w ? s_sum[e0 + i] : 0.0f) + sum_p[i];
+            for (int i = 0; i < V; i += 4) {
+                const int e = expert_of<L>(sub, i);
+                if (e < E4)
+                    *reinterpret_cast<f32x4*>(&s_sum[(int)threadIdx.x / kWave * E4 + e]) =
+                        f32x4{sum_p[i], sum_p[i + 1], sum_p[i + 2], sum_p[i + 3]};
             }
-            __syncthreads();
         }
-        for (int e = (int)threadIdx.x; e < a.E; e += 256) {
-            a.part_p[(int64_t)blockIdx.x * a.E + e] = s_sum[e];
+        __syncthreads();
+        for (int e = (int)threadIdx.x; e < a.E; e += kThreads) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kThreads / kWave; ++w) sum += s_sum[w * E4 + e];
+            a.part_p[(int64_t)blockIdx.x * a.E + e] = sum;
             a.part_n[(int64_t)blockIdx.x * a.E + e] = s_gate[e];
         }
         __syncthreads();
@@ -195,16 +261,17 @@ struct GateSumArgs {
 // Sums the first kernel's partials over its workgroups, kGateCols experts a
 // workgroup; the last workgroup to arrive adds the experts' shares of the loss
 // in their order.
-__global__ __launch_bounds__(256) void gate_sum_kernel(GateSumArgs a) {
-    __shared__ double s_p[4][kGateCols];
-    __shared__ int32_t s_n[4][kGateCols];
+__global__ __launch_bounds__(1024) void gate_sum_kernel(GateSumArgs a) {
+    __shared__ double s_p[16][kGateCols];
+    __shared__ int32_t s_n[16][kGateCols];
     __shared__ int s_last;
     const int c = lane_id(), g = (int)threadIdx.x / kWave;
     const int e = (int)blockIdx.x * kGateCols + c;
     double p = 0.0;
     int32_t n = 0;
     if (e < a.E)
-        for (int b = g; b < a.blocks; b += 4) {
+#pragma unroll 8
+        for (int b = g; b < a.blocks; b += 16) {
             p += (double)a.part_p[(int64_t)b * a.E + e];
             n += a.part_n[(int64_t)b * a.E + e];
         }
@@ -212,19 +279,19 @@ __global__ __launch_bounds__(256) void gate_sum_kernel(GateSumArgs a) {
     s_n[g][c] = n;
     __syncthreads();
     if (g == 0) {
-        p = ((s_p[0][c] + s_p[1][c]) + s_p[2][c]) + s_p[3][c];
-        n = s_n[0][c] + s_n[1][c] + s_n[2][c] + s_n[3][c];
+        for (int i = 1; i < 16; ++i) {
+            p += s_p[i][c];
+            n += s_n[i][c];
+        }
         if (e < a.E) a.num_tokens_per_expert[e] = n;
         double share = e < a.E ? p * (double)n : 0.0;
 #pragma unroll
         for (int o = 1; o < 64; o *= 2) share += __shfl_xor(share, o);
-        int last = 0;
         if (c == 0) {
             __hip_atomic_store(&a.part_loss[blockIdx.x], share, __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
-            last = __hip_atomic_fetch_add(a.arrive, 1u, __ATOMIC_ACQ_REL,
-                                          __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-            s_last = last;
+            s_last = __hip_atomic_fetch_add(a.arrive, 1u, __ATOMIC_ACQ_REL,
+                                            __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
         }
     }
     __syncthreads();
@@ -258,21 +325,26 @@ struct GateBackArgs {
     int32_t T, E, k, renorm;
 };
 
-template <typename F>
-__device__ inline void store_logit(void* p, int64_t i, float v);
-template <>
-__device__ inline void store_logit<float>(void* p, int64_t i, float v) {
-    reinterpret_cast<float*>(p)[i] = v;
-}
-template <>
-__device__ inline void store_logit<uint16_t>(void* p, int64_t i, float v) {
-    reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)bf16_pack(v, 0.0f);
+template <typename F, int L, int V, bool WIDE>
+__device__ inline void store_logits(void* p, int64_t base, int sub, int E, const float* v) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const int e = expert_of<L>(sub, i);
+        if constexpr (WIDE) {
+            if (e < E) Logits<F>::put4(p, base + e, v + i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (e + k < E) Logits<F>::put(p, base + e + k, v[i + k]);
+        }
+    }
 }
 
-template <typename F, int L, int V>
+template <typename F, int L, int V, bool WIDE>
 __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
     constexpr int kGroups = 256 / L;
-    const int sub = (int)threadIdx.x % L, e0 = sub * V;
+    constexpr int kHold = L == 16 ? 2 : 1;     // lane j of a group holds choices j and j + L
+    const int sub = (int)threadIdx.x % L;
     const int group0 = lane_id() & ~(L - 1);
     float d[V];
 #pragma unroll
@@ -281,33 +353,27 @@ __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
         const float n = fmaxf((float)a.num_tokens[0], 1.0f);
         const float c = a.grad_balance_loss[0] * (float)a.E / n / (n * (float)a.k);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e0 + i < a.E) d[i] = c * (float)a.num_tokens_per_expert[e0 + i];
+        for (int i = 0; i < V; ++i) {
+            const int e = expert_of<L>(sub, i);
+            if (e < a.E) d[i] = c * (float)a.num_tokens_per_expert[e];
+        }
     }
     for (int64_t t = (int64_t)blockIdx.x * kGroups + (int)threadIdx.x / L; t < a.T;
          t += (int64_t)gridDim.x * kGroups) {
         float p[V];
+        load_logits<F, L, V, WIDE>(a.logits, t * a.E, sub, a.E, p);   // under way with the mask
         if (a.mask && !a.mask[t]) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (e0 + i < a.E) store_logit<F>(a.grad_logits, t * a.E + e0 + i, 0.0f);
+            for (int i = 0; i < V; ++i) p[i] = 0.0f;
+            store_logits<F, L, V, WIDE>(a.grad_logits, t * a.E, sub, a.E, p);
             continue;
         }
-        load_logits<F, V>(a.logits, t * a.E, e0, a.E, p);
         const float lse = a.lse[t];
-        const float shift = lse == -__builtin_inff() ? 0.0f : lse;
-        float pd = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            p[i] = expf(p[i] - shift);
-            pd = fmaf(p[i], d[i], pd);
-        }
-        pd = group_sum<L>(pd);
-        float z[L == 16 ? 2 : 1], w[L == 16 ? 2 : 1];   // of choices sub and sub + L
-        int e[L == 16 ? 2 : 1];
+        float z[kHold], w[kHold];   // of choices sub and sub + L
+        int e[kHold];
         float S = 0.0f;
 #pragma unroll
-        for (int q = 0; q < (L == 16 ? 2 : 1); ++q) {
+        for (int q = 0; q < kHold; ++q) {
             const int j = sub + q * L;
             z[q] = w[q] = 0.0f;
             e[q] = -1;
@@ -319,24 +385,33 @@ __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
             S += z[q];
         }
         S = group_sum<L>(S);
+        const float shift = lse == -__builtin_inff() ? 0.0f : lse;
+        float pd = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = expf(p[i] - shift);
+            pd = fmaf(p[i], d[i], pd);
+        }
+        pd = group_sum<L>(pd);
         if (a.renorm)
 #pragma unroll
-            for (int q = 0; q < (L == 16 ? 2 : 1); ++q) z[q] = fmaf(-w[q], S, z[q]);
+            for (int q = 0; q < kHold; ++q) z[q] = fmaf(-w[q], S, z[q]);
         else
             pd += S;
         // p (d - pd), then each choice's part at its expert
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] *= d[i] - pd;
-        for (int j = 0; j < a.k; ++j) {
-            const bool high = j >= L;
-            const int ej = __shfl(high ? e[L == 16 ? 1 : 0] : e[0], group0 + j % L) - e0;
-            const float zj = __shfl(high ? z[L == 16 ? 1 : 0] : z[0], group0 + j % L);
+        if (a.grad_topk_w)
+            for (int j = 0; j < a.k; ++j) {
+                const bool high = j >= L;
+                const int ej = __shfl(high ? e[kHold - 1] : e[0], group0 + j % L);
+                const float zj = __shfl(high ? z[kHold - 1] : z[0], group0 + j % L);
+                // this lane's register of expert ej, if it has it
+                const int at = ej >= 0 && ej / 4 % L == sub ? ej / (4 * L) * 4 + ej % 4 : -1;
 #pragma unroll
-            for (int i = 0; i < V; ++i) p[i] += i == ej ? zj : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e0 + i < a.E) store_logit<F>(a.grad_logits, t * a.E + e0 + i, p[i]);
+                for (int i = 0; i < V; ++i) p[i] += i == at ? zj : 0.0f;
+            }
+        store_logits<F, L, V, WIDE>(a.grad_logits, t * a.E, sub, a.E, p);
     }
 }
 
@@ -346,7 +421,8 @@ int check_gate(int32_t T, int32_t E, int32_t k) {
     return EP_OK;
 }
 
-inline int gate_groups(int E) { return E <= 256 ? 16 : 4; }   // tokens of a workgroup at once
+// tokens that a workgroup of the call with counts has at once
+inline int gate_groups(int E) { return gate_threads(E) / (E <= 256 ? 16 : 64); }
 
 inline int64_t gate_blocks(int32_t T, int32_t E) {
     const int64_t b = ceil_div(T, gate_groups(E));
@@ -369,8 +445,6 @@ using namespace ep;
 namespace {
 // f(kernel of <float or bf16 bits, lanes, logits a lane>) for E experts.
 #define EP_GATE_SIZES(CALL)                                      \
-    if (E <= 16) return CALL(16, 1);                             \
-    if (E <= 32) return CALL(16, 2);                             \
     if (E <= 64) return CALL(16, 4);                             \
     if (E <= 128) return CALL(16, 8);                            \
     if (E <= 256) return CALL(16, 16);                           \
@@ -379,16 +453,22 @@ namespace {
     if (E <= 2048) return CALL(64, 32);                          \
     return CALL(64, 64)
 
-template <typename F, int L, int V>
+// Whether every token's logits can be read four at a time.
+template <typename F>
+bool wide_logits(const void* p, const void* q, int E) {
+    return E % 4 == 0 && (((uintptr_t)p | (uintptr_t)q) & (4 * sizeof(F) - 1)) == 0;
+}
+
+template <typename F, int L, int V, bool WIDE>
 int launch_gate_lv(const GateArgs& a, bool stats, hipStream_t stream) {
-    const int64_t all = ceil_div(a.T, 256 / L);
     clear_hip_error();
     if (stats)
-        hipLaunchKernelGGL((gate_kernel<F, L, V, true>), dim3((unsigned)gate_blocks(a.T, a.E)),
-                           dim3(256), (size_t)a.E * 8, stream, a);
+        hipLaunchKernelGGL((gate_kernel<F, L, V, WIDE, true>),
+                           dim3((unsigned)gate_blocks(a.T, a.E)), dim3(gate_threads(a.E)),
+                           (size_t)(a.E + 3) / 4 * 16 * (1 + gate_threads(a.E) / kWave), stream, a);
     else
-        hipLaunchKernelGGL((gate_kernel<F, L, V, false>), dim3((unsigned)all), dim3(256), 0,
-                           stream, a);
+        hipLaunchKernelGGL((gate_kernel<F, L, V, WIDE, false>),
+                           dim3((unsigned)ceil_div(a.T, 256 / L)), dim3(256), 0, stream, a);
     EP_HIP_CHECK(hipGetLastError());
     return EP_OK;
 }
@@ -396,15 +476,18 @@ int launch_gate_lv(const GateArgs& a, bool stats, hipStream_t stream) {
 template <typename F>
 int launch_gate(const GateArgs& a, bool stats, hipStream_t stream) {
     const int E = a.E;
-#define EP_CALL(L, V) launch_gate_lv<F, L, V>(a, stats, stream)
+    const bool wide = wide_logits<F>(a.logits, nullptr, E);
+#define EP_CALL(L, V)                                                  \
+    (wide ? launch_gate_lv<F, L, V, true>(a, stats, stream)            \
+          : launch_gate_lv<F, L, V, false>(a, stats, stream))
     EP_GATE_SIZES(EP_CALL);
 #undef EP_CALL
 }
 
-template <typename F, int L, int V>
+template <typename F, int L, int V, bool WIDE>
 int launch_gate_back_lv(const GateBackArgs& a, hipStream_t stream) {
     clear_hip_error();
-    hipLaunchKernelGGL((gate_back_kernel<F, L, V>), dim3((unsigned)ceil_div(a.T, 256 / L)),
+    hipLaunchKernelGGL((gate_back_kernel<F, L, V, WIDE>), dim3((unsigned)ceil_div(a.T, 256 / L)),
                        dim3(256), 0, stream, a);
     EP_HIP_CHECK(hipGetLastError());
     return EP_OK;
@@ -413,7 +496,10 @@ int launch_gate_back_lv(const GateBackArgs& a, hipStream_t stream) {
 template <typename F>
 int launch_gate_back(const GateBackArgs& a, hipStream_t stream) {
     const int E = a.E;
-#define EP_CALL(L, V) launch_gate_back_lv<F, L, V>(a, stream)
+    const bool wide = wide_logits<F>(a.logits, a.grad_logits, E);
+#define EP_CALL(L, V)                                                  \
+    (wide ? launch_gate_back_lv<F, L, V, true>(a, stream)              \
+          : launch_gate_back_lv<F, L, V, false>(a, stream))
     EP_GATE_SIZES(EP_CALL);
 #undef EP_CALL
 }
@@ -476,7 +562,7 @@ extern "C" int ep_route(int32_t T, int32_t E, int32_t k, int32_t dtype, int32_t 
     b.blocks = (int32_t)blocks;
     b.E = E;
     b.k = k;
-    hipLaunchKernelGGL(gate_sum_kernel, dim3((unsigned)sum_blocks(E)), dim3(256), 0, stream, b);
+    hipLaunchKernelGGL(gate_sum_kernel, dim3((unsigned)sum_blocks(E)), dim3(1024), 0, stream, b);
     EP_HIP_CHECK(hipGetLastError());
     return EP_OK;
 }

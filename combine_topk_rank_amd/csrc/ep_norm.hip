@@ -237,20 +237,27 @@ __global__ __launch_bounds__(1024) void norm_back_kernel(NormBackArgs a) {
     }
 }
 
-// Column sums of `part` [n, H] in a fixed order: 16 threads of 4 columns, 16
+// Column sums of `part` [n, H] in a fixed order: 16 threads of 4 columns, 64
 // slices of the rows, joined in LDS.
-__global__ __launch_bounds__(256) void norm_weight_kernel(const f32x4* part, int n, int H4,
-                                                          f32x4* out) {
-    __shared__ f32x4 s[16][16];
+__global__ __launch_bounds__(1024) void norm_weight_kernel(const f32x4* part, int n, int H4,
+                                                           f32x4* out) {
+    __shared__ f32x4 s[64][16];
     const int c = (int)threadIdx.x % 16, g = (int)threadIdx.x / 16;
     const int col = (int)blockIdx.x * 16 + c;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (col < H4)
-        for (int b = g; b < n; b += 16) v += part[(int64_t)b * H4 + col];
+#pragma unroll 8
+        for (int b = g; b < n; b += 64) v += part[(int64_t)b * H4 + col];
     s[g][c] = v;
     __syncthreads();
+    if (g < 8) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += s[g + 8 * i][c];
+        s[g][c] = v;
+    }
+    __syncthreads();
     if (g == 0 && col < H4) {
-        for (int i = 1; i < 16; ++i) v += s[i][c];
+        for (int i = 1; i < 8; ++i) v += s[i][c];
         out[col] = v;
     }
 }
@@ -369,7 +376,7 @@ extern "C" int ep_rmsnorm_backward(int32_t T, int32_t H, const void* r, const fl
                            : launch_norm_back<4>(a, blocks, stream);
         if (v != EP_OK) return v;
     }
-    hipLaunchKernelGGL(norm_weight_kernel, dim3((unsigned)ceil_div(H4, 16)), dim3(256), 0, stream,
+    hipLaunchKernelGGL(norm_weight_kernel, dim3((unsigned)ceil_div(H4, 16)), dim3(1024), 0, stream,
                        reinterpret_cast<const f32x4*>(workspace), blocks, H4,
                        reinterpret_cast<f32x4*>(grad_weight));
     EP_HIP_CHECK(hipGetLastError());

@@ -79,20 +79,46 @@ __device__ inline float amax8(const float* v) {
     return m;
 }
 
-// Reductions over aligned groups of N lanes (N a power of two), the result in
-// every lane of the group.
-template <int N>
-__device__ inline float group_max(float v) {
-#pragma unroll
-    for (int o = 1; o < N; o *= 2) v = fmaxf(v, __shfl_xor(v, o));
+// Reductions over aligned groups of N = 16 or 64 lanes, the result in every lane
+// of the group: within 16 lanes by data-parallel moves (neighbours, pairs, then
+// mirrored in 8 and in 16), across them by the row swaps of gfx950.
+template <int CTRL>
+__device__ inline uint32_t dpp_move(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+template <int N, typename T, typename OP>
+__device__ inline T group_reduce(T v, OP op) {
+    static_assert((N == 16 || N == 64) && sizeof(T) == 4, "groups of 16 or 64 lanes");
+    const auto step = [&](uint32_t other) { v = op(v, __builtin_bit_cast(T, other)); };
+    step(dpp_move<0xB1>(__builtin_bit_cast(uint32_t, v)));    // quad_perm 1 0 3 2
+    step(dpp_move<0x4E>(__builtin_bit_cast(uint32_t, v)));    // quad_perm 2 3 0 1
+    step(dpp_move<0x141>(__builtin_bit_cast(uint32_t, v)));   // row_half_mirror
+    step(dpp_move<0x140>(__builtin_bit_cast(uint32_t, v)));   // row_mirror
+    if constexpr (N == 64) {
+        uint32_t u = __builtin_bit_cast(uint32_t, v);
+        u32x2 p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        v = op(__builtin_bit_cast(T, (uint32_t)p[0]), __builtin_bit_cast(T, (uint32_t)p[1]));
+        u = __builtin_bit_cast(uint32_t, v);
+        p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        v = op(__builtin_bit_cast(T, (uint32_t)p[0]), __builtin_bit_cast(T, (uint32_t)p[1]));
+    }
     return v;
 }
 
 template <int N>
+__device__ inline float group_max(float v) {
+    return group_reduce<N>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+template <int N>
 __device__ inline float group_sum(float v) {
-#pragma unroll
-    for (int o = 1; o < N; o *= 2) v += __shfl_xor(v, o);
-    return v;
+    return group_reduce<N>(v, [](float a, float b) { return a + b; });
+}
+
+template <int N>
+__device__ inline int group_min(int v) {
+    return group_reduce<N>(v, [](int a, int b) { return a < b ? a : b; });
 }
 
 }  // namespace ep

@@ -135,6 +135,11 @@ def test_too_many_tiles_is_refused(ep):
     assert b"tiles" in ep.lib.ep_last_error()
 
 
+def test_row_bytes_of_the_binding(ep):
+    for H in [128 * i for i in range(1, 200)] + [1 << 20]:
+        assert ep._row8(H) == ep.ep_row_bytes(H, ep.EP_FMT_FP8_E4M3_B128)
+
+
 def test_python_names_a_wrong_tensor(ep):
     """The binding's own checks, on tensors of the CPU: the current device is
     taken as theirs (-1)."""
