@@ -114,6 +114,13 @@ void record_error(const char* what);
 // left by unrelated earlier calls of the thread: clear it before a launch.
 inline void clear_hip_error() { (void)hipGetLastError(); }
 
+// Workgroups of a kernel that loops over its work: `n`, but no more than keep
+// the grid's threads within 2^31 (a launch takes fewer than 2^32).
+inline unsigned loop_grid(int64_t n, int threads) {
+    const int64_t most = ((int64_t)1 << 31) / threads;
+    return (unsigned)(n < most ? n : most);
+}
+
 // First error wins.
 __device__ inline void set_error(int32_t* st, int code) {
     atomicCAS(st, 0, code);

@@ -698,30 +698,31 @@ int expert_args(ExpertArgs& a, int32_t G, int64_t M, int32_t N, int32_t K, const
     return EP_OK;
 }
 
-// Workgroups of a launch: one for each column tile of the row tiles that there
-// can be, or, `most` > 0, that many at most, a multiple of the eight XCDs, which
-// share the tiles out.
-int grid_of(const ExpertArgs& a, int bm, int most, unsigned* blocks) {
-    int64_t n = max_tiles(a.M, a.G, bm) * a.n_tiles;
+// Whether tiles of 16 rows, a workgroup each, fit a launch's 2^31 threads.
+bool small_fits(const ExpertArgs& a, int threads) {
+    return max_tiles(a.M, a.G, 16) * a.n_tiles <= ((int64_t)1 << 31) / threads;
+}
+
+#define EP_LAUNCH_EXPERT(KERNEL, BLOCKS, THREADS)                                             \
+    do {                                                                                      \
+        clear_hip_error();                                                                    \
+        hipLaunchKernelGGL((KERNEL), dim3((unsigned)(BLOCKS)), dim3(THREADS), 0, stream, a);  \
+        EP_HIP_CHECK(hipGetLastError());                                                      \
+        return EP_OK;                                                                         \
+    } while (0)
+
+// Big tiles: a workgroup a CU, or, for fewer tiles, one each, in whole eights
+// for the XCDs that share them out.
+template <bool GATE>
+int launch_big(const ExpertArgs& a, hipStream_t stream) {
+    const int64_t n = max_tiles(a.M, a.G, kBigRows) * a.n_tiles;
     if (n >= ((int64_t)1 << 31)) {
         record_error("expert product: more than 2^31 tiles");
         return EP_ERR_INVALID_ARG;
     }
-    if (most > 0) n = n < most ? ceil_div(n, 8) * 8 : most;
-    *blocks = (unsigned)n;
-    return EP_OK;
+    EP_LAUNCH_EXPERT(product_big_kernel<GATE>, n < kBigGrid ? ceil_div(n, 8) * 8 : kBigGrid,
+                     kBigThreads);
 }
-
-#define EP_LAUNCH_TILES(KERNEL, BM, THREADS, MOST)                                            \
-    do {                                                                                   \
-        unsigned blocks = 0;                                                               \
-        const int v_ = grid_of(a, BM, MOST, &blocks);                                      \
-        if (v_ != EP_OK) return v_;                                                        \
-        clear_hip_error();                                                                 \
-        hipLaunchKernelGGL((KERNEL), dim3(blocks), dim3(THREADS), 0, stream, a);           \
-        EP_HIP_CHECK(hipGetLastError());                                                   \
-        return EP_OK;                                                                      \
-    } while (0)
 }  // namespace
 
 extern "C" int ep_expert_product(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
@@ -734,17 +735,16 @@ extern "C" int ep_expert_product(int32_t G, int64_t M, int32_t N, int32_t K, con
     if (v != EP_OK) return v;
     if (M == 0) return EP_OK;
     a.out_bytes = 2 * N;
-    a.n_tiles = (int32_t)ceil_div(N, 16);
     // Rows a group, were they even.  Big tiles against small, us, unequal counts:
     // 24 experts, 2176 x 896: 15.5 : 15.0 at 8 rows a group, 17.0 : 20.7 at 16;
     // 8 experts, 7168 x 1792: 29.3 : 29.6 and 30.2 : 40.6; fewer rows are the
     // small tiles', more the big ones'.
     const int64_t per = ceil_div(M, G);
-    if (per > 8) {
-        a.n_tiles = (int32_t)ceil_div(N, kBigRows);
-        EP_LAUNCH_TILES(product_big_kernel<false>, kBigRows, kBigThreads, kBigGrid);
-    }
-    EP_LAUNCH_TILES(product_small_kernel, 16, 256, 0);
+    a.n_tiles = (int32_t)ceil_div(N, 16);
+    if (per <= 8 && small_fits(a, 256))
+        EP_LAUNCH_EXPERT(product_small_kernel, max_tiles(M, G, 16) * a.n_tiles, 256);
+    a.n_tiles = (int32_t)ceil_div(N, kBigRows);
+    return launch_big<false>(a, stream);
 }
 
 extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, const void* rows,
@@ -762,6 +762,7 @@ extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, con
     // As above, us: 24 experts, 2176 x 896: 39.8 : 37.2 at 16 rows a group, 43.5 :
     // 62.7 at 24; 8 experts, 7168 x 1792: 96.8 : 79.9 and 102 : 82.0.
     const int64_t per = ceil_div(M, G);
-    if (per > 16) EP_LAUNCH_TILES(product_big_kernel<true>, kBigRows, kBigThreads, kBigGrid);
-    EP_LAUNCH_TILES(gate_up_small_kernel, 16, 1024, 0);
+    if (per <= 16 && small_fits(a, 1024))
+        EP_LAUNCH_EXPERT(gate_up_small_kernel, max_tiles(M, G, 16) * a.n_tiles, 1024);
+    return launch_big<true>(a, stream);
 }

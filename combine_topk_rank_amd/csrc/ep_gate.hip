@@ -468,7 +468,7 @@ int launch_gate_lv(const GateArgs& a, bool stats, hipStream_t stream) {
                            (size_t)(a.E + 3) / 4 * 16 * (1 + gate_threads(a.E) / kWave), stream, a);
     else
         hipLaunchKernelGGL((gate_kernel<F, L, V, WIDE, false>),
-                           dim3((unsigned)ceil_div(a.T, 256 / L)), dim3(256), 0, stream, a);
+                           dim3(loop_grid(ceil_div(a.T, 256 / L), 256)), dim3(256), 0, stream, a);
     EP_HIP_CHECK(hipGetLastError());
     return EP_OK;
 }
@@ -487,8 +487,8 @@ int launch_gate(const GateArgs& a, bool stats, hipStream_t stream) {
 template <typename F, int L, int V, bool WIDE>
 int launch_gate_back_lv(const GateBackArgs& a, hipStream_t stream) {
     clear_hip_error();
-    hipLaunchKernelGGL((gate_back_kernel<F, L, V, WIDE>), dim3((unsigned)ceil_div(a.T, 256 / L)),
-                       dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((gate_back_kernel<F, L, V, WIDE>),
+                       dim3(loop_grid(ceil_div(a.T, 256 / L), 256)), dim3(256), 0, stream, a);
     EP_HIP_CHECK(hipGetLastError());
     return EP_OK;
 }

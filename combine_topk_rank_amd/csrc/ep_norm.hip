@@ -287,8 +287,8 @@ int launch_norm(const NormArgs& a, hipStream_t stream) {
     const int64_t blocks = ceil_div(a.T, rpb);
     const int threads = TPR ? 256 : row_threads(a.nv, V);
     clear_hip_error();
-    hipLaunchKernelGGL((norm_kernel<V, TPR>), dim3((unsigned)blocks), dim3((unsigned)threads), 0,
-                       stream, a);
+    hipLaunchKernelGGL((norm_kernel<V, TPR>), dim3(loop_grid(blocks, threads)),
+                       dim3((unsigned)threads), 0, stream, a);
     EP_HIP_CHECK(hipGetLastError());
     return EP_OK;
 }

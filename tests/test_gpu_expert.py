@@ -18,10 +18,12 @@ pytestmark = pytest.mark.gpu
 PRODUCT = [([1], 8, 128), ([1], 16, 256), ([3], 24, 384), ([16], 128, 128), ([17], 136, 512), ([0, 5, 0, 1], 64, 128),
            ([2, 0, 31, 7], 264, 640), ([1] * 70, 40, 128), ([0] * 65 + [4], 72, 256), ([33, 64, 65], 200, 384),
            ([128, 127, 129, 0, 1], 512, 512), ([300], 1000, 896), ([255, 257, 0, 513], 520, 1792),
-           ([40, 1000, 3], 1208, 256), ([700], 256, 128)]
+           ([40, 1000, 3], 1208, 256), ([700], 256, 128), ([300], 8, 128),
+           ([20, 19, 64, 1], 40, 384), ([530], 304, 640), ([9] * 40, 264, 256), ([8] * 33 + [250], 376, 512)]
 GATE_UP = [([1], 128, 128), ([3], 128, 256), ([16, 17], 256, 384), ([0, 5, 0, 1], 384, 128), ([2, 0, 31, 7], 128, 640),
            ([1] * 70, 128, 128), ([33, 64, 65], 256, 384), ([128, 127, 129, 0, 1], 640, 512), ([300], 896, 896),
-           ([255, 257, 0, 513], 128, 1792), ([40, 1000, 3], 384, 256)]
+           ([255, 257, 0, 513], 128, 1792), ([40, 1000, 3], 384, 256), ([16] * 5, 128, 2304),
+           ([15, 17, 1], 256, 2176), ([11], 128, 4096), ([600], 128, 128), ([17] * 40, 256, 256)]
 
 
 @pytest.fixture(scope="module")
@@ -213,6 +215,34 @@ def test_bad_offsets_are_reported(ep):
     out, st = product(ep, rows, [0, 10, 20, 51], w, sw, M, N)
     assert st == 3
     assert torch.equal(out[:20], R.grouped64(x, [0, 10, 20, 50], w64)[:20].float().bfloat16())
+
+
+@pytest.mark.parametrize("which", ["product", "gate_up"])
+def test_many_tiles_a_workgroup(ep, which):
+    """More tiles than the GPU has CUs, so that workgroups go from one to the
+    next: whole, ragged and short ones of several groups."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    counts, K = [1000, 0, 256, 3, 2817, 511], 256
+    off = offsets(counts, 2)
+    M = off[-1] + 5
+    N = 5896 if which == "product" else 2 * 2944
+    rows, x, w, sw, w64 = exact_inputs(M, len(counts), N, K, gen)
+    inside = slice(2, off[-1])
+    for _ in range(2):
+        if which == "product":
+            out, st = product(ep, rows, off, w, sw, M, N)
+            want = R.grouped64(x, off, w64)
+            assert torch.equal(out[inside], want[inside].float().bfloat16())
+            assert (out[:2] == -7).all() and (out[off[-1]:] == -7).all()
+        else:
+            out, st = gate_up(ep, rows, off, w, sw * 2.0 ** -6, M, N // 2)
+            y = R.grouped64(x, off, w64 * 2.0 ** -6)[inside]
+            g, u = y[:, :N // 2], y[:, N // 2:]
+            h = g / (1 + torch.exp(-g)) * u
+            big = g.abs().view(g.shape[0], -1, 128).amax(2)
+            R.assert_rows8(out[inside], h, (big + 6) * R.U32, "out_rows")
+            assert (out[:2] == 0xA5).all() and (out[off[-1]:] == 0xA5).all()
+        assert st == 0
 
 
 def test_weights_as_float8_and_many_groups(ep):

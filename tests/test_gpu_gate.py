@@ -261,6 +261,18 @@ def test_one_workspace_many_calls_and_a_graph(ep):
         check(forward(ep, l2, m2, k, 0, ws=ws), l2, m2, k, 0)
 
 
+@pytest.mark.parametrize("half", [False, True])
+def test_logits_that_lie_between_words(ep, half):
+    """Logits behind an odd offset: aligned to their type alone."""
+    T, E, k = 65, 64, 4
+    base, _ = make(1, T * E + 1, half, 18)
+    logits = base[0, 1:].view(T, E)
+    o = forward(ep, logits, None, k, 1)
+    check(o, logits, None, k, 1)
+    gw = torch.ones(T, k, device="cuda")
+    check_back(backward(ep, logits, None, 1, o, gw, None), logits, None, k, 1, gw, None)
+
+
 def test_other_stream(ep):
     logits, mask = make(1000, 256, True, 16, True)
     s = torch.cuda.Stream()
