@@ -170,17 +170,18 @@ __device__ inline void store_block(const ExpertArgs& a, int64_t m, int fb, const
 
 // Few rows a group, with the gate: a workgroup has the 128 gates and 128 ups
 // of one output block and 16 rows; wavefront w has 16 of those weight rows over
-// all of K.  Weights go from memory to registers, four blocks (8 KB a wavefront)
-// under way; the 16 wavefronts share the rows through LDS, sixteen blocks at a
-// time and the next sixteen under way, since a CU takes no more than about 25
-// GB/s in all (reading the rows once a wavefront: 118 against 73 us for 4 rows
-// against one at each of 8 experts, 7168 x 1792).
+// all of K.  Weights go from memory to registers, a block ahead; the 16
+// wavefronts share the rows through LDS, sixteen blocks at a time and the next
+// sixteen under way, since a CU takes in no more than about 25 GB/s: with rows
+// read once a wavefront, 4 rows at each of 8 experts, 7168 x 1792, took 118 us
+// and one row 73.  Now 66 and 65 (3.2 TB/s: 112 of the 256 CUs have work); 24
+// experts of 2176 x 896 take 20 us (4.6 TB/s).  One block ahead, two workgroups
+// a CU: with two or four ahead, and fewer wavefronts, 25 and 32 us.
 constexpr int kSlab = 16;                              // blocks of K of the rows in LDS
 constexpr int kSlabPitch = kSlab * kScaleBlock + 16;   // 16 rows' reads meet all banks once
 
 __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
     constexpr int kPitch = 2 * kScaleBlock + 4;
-    constexpr int kAhead = 4;
     __shared__ __attribute__((aligned(16))) uint8_t s_x[2][16][kSlabPitch];
     __shared__ float s_sx[2][16][kSlab];
     static_assert(sizeof(float) * 16 * kPitch <= sizeof s_x, "the outputs reuse the rows' LDS");
@@ -191,9 +192,11 @@ __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
     if (tile.g < 0) return;
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = tid / kWave;
     const int F = a.N / 2, nb = a.K / kScaleBlock;
-    const int n0 = (wave < 8 ? 0 : F) + fb * kScaleBlock + wave % 8 * 16;
-    const uint8_t* wrow =
-        a.w + ((int64_t)tile.g * a.N + n0 + lane % 16) * a.K + lane / 16 * 16;
+    const int n0 = __builtin_amdgcn_readfirstlane((wave < 8 ? 0 : F) + fb * kScaleBlock + wave % 8 * 16);
+    // 16 rows of at most 2^20 bytes
+    const __amdgpu_buffer_rsrc_t wbuf =
+        buffer_rsrc(const_cast<uint8_t*>(a.w) + ((int64_t)tile.g * a.N + n0) * a.K, 16 * a.K);
+    const uint32_t wat = (uint32_t)(lane % 16) * a.K + lane / 16 * 16;
     const float* sw = a.w_scale + ((int64_t)tile.g * (a.N / 128) + n0 / 128) * nb;
 
     // this thread's part of a slab: 32 bytes of one row, and a scale of 256
@@ -215,29 +218,25 @@ __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
         if (sc % 4 == 0) s_sx[to][sr][sc / 4] = part_scale;
     };
 
-    i32x8 w[kAhead];
-    float s[kAhead];
-    const auto load = [&](int d, int b) {
-        b = b < nb ? b : nb - 1;
-        w[d] = join(load16(wrow + b * kScaleBlock), load16(wrow + b * kScaleBlock + 64));
-        s[d] = sw[b];
+    i32x8 w;
+    float s;
+    const auto load = [&](int b) {
+        const int k = b * kScaleBlock;
+        w = join(__builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat, k, 0)),
+                 __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat + 64, k, 0)));
+        s = sw[b];
     };
     read_slab(0);
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) load(d, d);
+    load(0);
     write_slab(0);
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     const uint8_t* lx = nullptr;
     const float* lsx = nullptr;
-    const auto use = [&](int d, int c) {
+    const auto use = [&](int c) {
         const i32x8 x = join(load16(lx + c * kScaleBlock), load16(lx + c * kScaleBlock + 64));
-        acc = fma4(mfma16(w[d], x), s[d] * lsx[c], acc);
+        acc = fma4(mfma16(w, x), s * lsx[c], acc);
     };
-    // four blocks a step, those of the next step read behind them; the last
-    // step reads none (no load hides behind a branch, or the compiler would wait
-    // for all that are under way)
-    const int last = (nb - 1) / kAhead * kAhead;
-    for (int b = 0; b < last; b += kAhead) {
+    for (int b = 0; b < nb; ++b) {
         const int c = b % kSlab, turn = b / kSlab % 2;
         if (c == 0) {
             __syncthreads();
@@ -245,21 +244,12 @@ __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
             lsx = s_sx[turn][lane % 16];
             if (b + kSlab < nb) read_slab(b + kSlab);
         }
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-            use(d, c + d);
-            load(d, b + kAhead + d);
+        use(c);
+        if (b + 1 < nb) {
+            load(b + 1);
+            if (c == kSlab - 1) write_slab(turn ^ 1);
         }
-        if (c == kSlab - kAhead && b + kAhead < nb) write_slab(turn ^ 1);
     }
-    if (last % kSlab == 0) {
-        __syncthreads();
-        lx = &s_x[last / kSlab % 2][lane % 16][lane / 16 * 16];
-        lsx = s_sx[last / kSlab % 2][lane % 16];
-    }
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-        if (last + d < nb) use(d, last % kSlab + d);
     __syncthreads();
     *reinterpret_cast<f32x4*>(&s_y[lane % 16][wave * 16 + lane / 16 * 4]) = acc;
     __syncthreads();
@@ -329,7 +319,9 @@ __device__ inline int64_t count_tiles(const int32_t* off, int G, int64_t M, int 
 
 // A workgroup's share of the tiles.  Workgroups go to the eight XCDs in turn:
 // each XCD gets one run of the tiles, ordered so that the 32 it has at a time
-// are 4 row tiles x 8 column tiles, whose operands its L2 shares.
+// are 5 row tiles x 6 or 7 column tiles, whose operands its L2 shares (8192 x
+// 8192 x 7168: 480 us against 486, 496, 486, 500 for 3, 4, 6 and 8).
+constexpr int kBand = 5;
 struct TileShare {
     int64_t row_tiles, first;   // first: this workgroup's; the next ones follow `step` apart
     int32_t count, step, n_tiles;
@@ -347,12 +339,12 @@ struct TileShare {
 
     // row tile and column tile of the workgroup's i-th tile
     __device__ void place(int i, int64_t* m, int* n) const {
-        const int64_t at = first + (int64_t)i * step, wide = 4 * (int64_t)n_tiles;
+        const int64_t at = first + (int64_t)i * step, wide = kBand * (int64_t)n_tiles;
         const int64_t band = at / wide;
         const int in = (int)(at - band * wide);
-        const int64_t left = row_tiles - band * 4;
-        const int rows = (int)(left < 4 ? left : 4);
-        *m = band * 4 + in % rows;
+        const int64_t left = row_tiles - band * kBand;
+        const int rows = (int)(left < kBand ? left : kBand);
+        *m = band * kBand + in % rows;
         *n = in / rows;
     }
 };
@@ -759,10 +751,10 @@ extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, con
     if (M == 0) return EP_OK;
     a.out_bytes = (int32_t)row_bytes(F, EP_FMT_FP8_E4M3_B128);
     a.n_tiles = F / kScaleBlock;
-    // As above, us: 24 experts, 2176 x 896: 39.8 : 37.2 at 16 rows a group, 43.5 :
-    // 62.7 at 24; 8 experts, 7168 x 1792: 96.8 : 79.9 and 102 : 82.0.
+    // As above, us: 24 experts, 2176 x 896: 44.9 : 41.0 at 32 rows a group, 48.4 :
+    // 55.7 at 48; 8 experts, 7168 x 1792: 105 : 83 and 111 : 116.
     const int64_t per = ceil_div(M, G);
-    if (per <= 16 && small_fits(a, 1024))
+    if (per <= 32 && small_fits(a, 1024))
         EP_LAUNCH_EXPERT(gate_up_small_kernel, max_tiles(M, G, 16) * a.n_tiles, 1024);
     return launch_big<true>(a, stream);
 }
