@@ -18,8 +18,10 @@
 // The choices are k rounds of a maximum over the group (exact in float), then
 // of the lowest expert that has it.
 //
-// Bound: 16384 tokens of 256 experts are 16.8 MB of logits, 3.4 us at a copy's
+// 16384 tokens of 256 experts, k = 8, are 16.8 MB of logits, 3.4 us at a copy's
 // rate; the k rounds cost about 90 instructions for four tokens each, 6 us.
+// With counts and loss: 17 us and 6 of the second kernel; backward 16 us (16
+// lanes a token with one logit a load: 36, 22 and 37 us).
 
 #include "ep_rows8.h"
 

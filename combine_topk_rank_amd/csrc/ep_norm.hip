@@ -14,7 +14,10 @@
 //   grad_weight = sum over rows of grad_y * h
 //
 // Both are bound by memory: a row is read once into registers, its sum taken
-// across the row's threads, and written once.
+// across the row's threads, and written once.  16384 x 7168 with a residual,
+// bf16 and 8-bit outputs (1.06 GB): 194 us, 5.5 TB/s; the backward of 4096 x 7168
+// with a residual's gradient (235 MB): 49 us, 4.8 TB/s, and 5 us for the sum of
+// the weight gradient's parts.
 
 #include "ep_rows8.h"
 
