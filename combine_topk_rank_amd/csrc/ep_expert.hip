@@ -650,6 +650,180 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs 
     wait_vm();   // no copy may reach the LDS after the workgroup's end
 }
 
+// ---- Some rows a group ----------------------------------------------------------
+// 256 weight rows x up to 64 rows a workgroup: a wavefront has 32 of the weight
+// rows (for the gate: 16 gates and their ups) and all the rows.  Four blocks of
+// K of both operands, 40 KB each, fill the LDS, three of them under way.
+constexpr int kMidRows = 64;
+constexpr int kMidStages = 4;
+constexpr int kMidBytes = kOperandBytes + kMidRows * kScaleBlock;
+
+template <bool GATE>
+__global__ __launch_bounds__(kBigThreads, 2) void product_mid_kernel(ExpertArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[kMidStages * kMidBytes];
+    if (blockIdx.x == 0) check_groups(a);
+    const int nt = (int)(blockIdx.x % (unsigned)a.n_tiles);
+    const RowTile tile =
+        find_tile(a.group_offset, a.G, a.M, blockIdx.x / (unsigned)a.n_tiles, kMidRows);
+    if (tile.g < 0) return;
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int nb = a.K / kScaleBlock, F = a.N / 2;
+
+    // Copies: four parts of 8 weight rows and one of 8 rows a wavefront, chunks
+    // and buffers' ends as in the big tiles.  wbuf: this wavefront's weight rows,
+    // for the gate its gates and its ups.
+    constexpr int kHalves = GATE ? 2 : 1;
+    __amdgpu_buffer_rsrc_t wbuf[kHalves];
+    uint32_t osw[kHalves];      // this wavefront's row of the weights' scales
+    const int scale_rows = (a.N + 127) / 128;
+    const __amdgpu_buffer_rsrc_t swbuf = buffer_rsrc(
+        const_cast<float*>(a.w_scale) + (int64_t)tile.g * scale_rows * nb, scale_rows * nb * 4);
+    if constexpr (GATE) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = h * F + nt * 128 + wave * 16;
+            wbuf[h * (kHalves - 1)] = buffer_rsrc(
+                const_cast<uint8_t*>(a.w) + ((int64_t)tile.g * a.N + n) * a.K, 16 * a.K);
+            osw[h * (kHalves - 1)] = (uint32_t)((h * F / 128 + nt) * nb) * 4;
+        }
+    } else {
+        const int n0 = nt * kBigRows + wave * 32, base = n0 < a.N ? n0 : a.N - 1;
+        const int rows = a.N - base < 32 ? a.N - base : 32;
+        wbuf[0] = buffer_rsrc(const_cast<uint8_t*>(a.w) + ((int64_t)tile.g * a.N + base) * a.K,
+                              rows * a.K);
+        osw[0] = (uint32_t)(base / 128 * nb) * 4;
+    }
+    const __amdgpu_buffer_rsrc_t xbuf = buffer_rsrc(
+        const_cast<uint8_t*>(a.rows) + tile.first * a.row_bytes, tile.count * a.row_bytes);
+    // row q of a part sits with its chunk c at c ^ (row of the operand / 2 % 8)
+    const uint32_t ow = (uint32_t)(lane / 8) * a.K + ((lane % 8) ^ (lane / 16)) * 16;
+    const uint32_t ox = (uint32_t)(wave * 8 + lane / 8) * a.row_bytes +
+                        ((lane % 8) ^ ((wave * 4 + lane / 16) % 8)) * 16;
+    const auto fetch = [&](int b) {
+        const int at = (b < nb ? b : nb - 1) * kScaleBlock;   // repeated behind the last block
+        uint8_t* l = s_mem + b % kMidStages * kMidBytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int half = GATE ? i / 2 : 0, part = GATE ? i % 2 : i;
+            to_lds(wbuf[half], (ow ^ (i % 2 * 64)) + (uint32_t)(part * 8) * a.K, at,
+                   l + wave * 4096 + i * 1024);
+        }
+        to_lds(xbuf, ox, at, l + kOperandBytes + wave * 1024);
+    };
+    const uint32_t osx = (uint32_t)(lane % 16) * a.row_bytes + a.K;
+    float sx[4], sw[kHalves];
+    const auto scales = [&](int b) {
+        const int at = (b < nb ? b : nb - 1) * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sx[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                xbuf, osx + (uint32_t)(j * 16) * a.row_bytes, at, 0));
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+            sw[h] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(swbuf, osw[h], at, 0));
+    };
+
+    f32x4 acc[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int at0 = lane % 16 * 128 + ((lane / 16 ^ (lane % 16 / 2)) * 16), at1 = at0 ^ 64;
+    fetch(0);
+    fetch(1);
+    __builtin_amdgcn_sched_barrier(0);
+    scales(0);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(2);
+    for (int b = 0; b < nb; ++b) {
+        // block b is here when all but the two copies behind it and the scales
+        // between them are; everyone is then done with block b - 1
+        meet<5 + 4 + kHalves + 5, 0>();
+        float s[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = sx[j] * sw[i * (kHalves - 1)];
+        // in this order, or waiting for the scales would be waiting for the copies
+        __builtin_amdgcn_sched_barrier(0);
+        scales(b + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(b + 3);
+        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t* l = s_mem + b % kMidStages * kMidBytes;
+        i32x8 w[2], x[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = join(load16(l + wave * 4096 + i * 2048 + at0),
+                        load16(l + wave * 4096 + i * 2048 + at1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[j] = join(load16(l + kOperandBytes + j * 2048 + at0),
+                        load16(l + kOperandBytes + j * 2048 + at1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) acc[i][j] = fma4(mfma16(w[i], x[j]), s[i][j], acc[i][j]);
+    }
+
+    const int r = lane % 16, g = lane / 16;
+    if constexpr (!GATE) {
+        wait_vm();   // no copy may reach the LDS after the workgroup's end
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // as in the big tiles: 8 columns of one of two neighbouring tiles
+            const u32x2 lo = __builtin_amdgcn_permlane16_swap(
+                bf16_pack(acc[0][j][0], acc[0][j][1]), bf16_pack(acc[1][j][0], acc[1][j][1]), false,
+                false);
+            const u32x2 hi = __builtin_amdgcn_permlane16_swap(
+                bf16_pack(acc[0][j][2], acc[0][j][3]), bf16_pack(acc[1][j][2], acc[1][j][3]), false,
+                false);
+            const int row = j * 16 + r, c = nt * kBigRows + wave * 32 + g % 2 * 16 + g / 2 * 8;
+            if (row < tile.count && c < a.N)
+                *reinterpret_cast<u32x4*>(a.out + (tile.first + row) * a.out_bytes + 2 * c) =
+                    u32x4{lo[0], hi[0], lo[1], hi[1]};
+        }
+    } else {
+        meet<0, 0>();    // the copies behind the last block are in, its reads done
+        float* const s_max = reinterpret_cast<float*>(s_mem);
+        float am[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            am[j] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                acc[0][j][q] = silu_mul(acc[0][j][q], acc[1][j][q]);
+                am[j] = fmaxf(am[j], fabsf(acc[0][j][q]));
+            }
+            am[j] = fmaxf(am[j], __shfl_xor(am[j], 16));
+            am[j] = fmaxf(am[j], __shfl_xor(am[j], 32));
+            if (g == 0) s_max[wave * kMidRows + j * 16 + r] = am[j];
+        }
+        __syncthreads();
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) am[j] = fmaxf(am[j], s_max[v * kMidRows + j * 16 + r]);
+            am[j] = fmaxf(am[j], kAmaxMin);
+            const float h[8] = {acc[0][j][0], acc[0][j][1], acc[0][j][2], acc[0][j][3],
+                                0.0f,         0.0f,         0.0f,         0.0f};
+            c[j] = fp8_pack8(h, kFp8Max / am[j])[0];
+        }
+        transpose4(c);   // this lane: the wavefront's 16 outputs of row 16 g + r
+        const float mine = g == 0 ? am[0] : g == 1 ? am[1] : g == 2 ? am[2] : am[3];
+        const int row = g * 16 + r;
+        if (row < tile.count) {
+            uint8_t* out = a.out + (tile.first + row) * a.out_bytes;
+            *reinterpret_cast<u32x4*>(out + nt * 128 + wave * 16) = u32x4{c[0], c[1], c[2], c[3]};
+            if (wave == 0) *reinterpret_cast<float*>(out + F + 4 * nt) = mine / kFp8Max;
+            if (nt == F / 128 - 1)
+                for (int o = F + F / 32 + 4 * wave; o < a.out_bytes; o += 32)
+                    *reinterpret_cast<uint32_t*>(out + o) = 0u;
+        }
+    }
+}
+
 // A tile's 256 rows stay within 32-bit offsets.
 constexpr int kMaxK8 = 1 << 20;
 
@@ -693,9 +867,16 @@ int expert_args(ExpertArgs& a, int32_t G, int64_t M, int32_t N, int32_t K, const
     return EP_OK;
 }
 
-// Whether tiles of 16 rows, a workgroup each, fit a launch's 2^31 threads.
-bool small_fits(const ExpertArgs& a, int threads) {
-    return max_tiles(a.M, a.G, 16) * a.n_tiles <= ((int64_t)1 << 31) / threads;
+// Whether tiles of bm rows, a workgroup each, fit a launch's 2^31 threads.
+bool tiles_fit(const ExpertArgs& a, int bm, int threads) {
+    return max_tiles(a.M, a.G, bm) * a.n_tiles <= ((int64_t)1 << 31) / threads;
+}
+
+// Whether the middle tiles can take it: a launch's threads, and one expert's
+// scales within a buffer's 2^31 bytes.
+bool mid_fits(const ExpertArgs& a) {
+    return tiles_fit(a, kMidRows, kBigThreads) &&
+           ceil_div(a.N, kScaleBlock) * (a.K / kScaleBlock) < ((int64_t)1 << 29);
 }
 
 #define EP_LAUNCH_EXPERT(KERNEL, BLOCKS, THREADS)                                             \
@@ -730,15 +911,24 @@ extern "C" int ep_expert_product(int32_t G, int64_t M, int32_t N, int32_t K, con
     if (v != EP_OK) return v;
     if (M == 0) return EP_OK;
     a.out_bytes = 2 * N;
-    // Rows a group, were they even.  Big tiles against small, us, unequal counts:
-    // 24 experts, 2176 x 896: 15.5 : 15.0 at 8 rows a group, 17.0 : 20.7 at 16;
-    // 8 experts, 7168 x 1792: 29.3 : 29.6 and 30.2 : 40.6; fewer rows are the
-    // small tiles', more the big ones'.
-    const int64_t per = ceil_div(M, G);
-    a.n_tiles = (int32_t)ceil_div(N, 16);
-    if (per <= 8 && small_fits(a, 256))
-        EP_LAUNCH_EXPERT(product_small_kernel, max_tiles(M, G, 16) * a.n_tiles, 256);
-    a.n_tiles = (int32_t)ceil_div(N, kBigRows);
+    // Small tiles where the weights pass once or twice whatever the tile (up to 2
+    // rows a group), where all tiles read little, or where middle tiles would
+    // leave most CUs idle; middle tiles up to 48 rows a group and while they go
+    // round the CUs once or so.  Small : middle : big, us, unequal counts:
+    //   1 row a group      8 experts, 7168 x 1792  20 : 21 : 28   32 of the same  69 : 82 : 102
+    //   8 rows             the same                30 : 22 : 29                  107 : 85 : 108
+    //   8 rows, 32 experts, 1024 x 512 (25 MB)    8.4 : 10 : 12   48 rows 18 : 12 : 18
+    //   64 rows, 1 expert, 7168 x 1792 (56 tiles)  17 : 22 : 22   128 rows 31 : 23 : 26
+    //   96 rows, 8 experts, 7168 x 1792 (560)     126 : 48 : 39   24 of 2176 x 896 62 : 29 : 24
+    const int64_t per = ceil_div(M, G);   // rows a group, were they even
+    const int64_t n_small = ceil_div(N, 16), n_big = ceil_div(N, kBigRows);
+    const int64_t read = max_tiles(M, G, 16) * N * K, mid = max_tiles(M, G, kMidRows) * n_big;
+    a.n_tiles = (int32_t)n_small;
+    if ((per <= 2 || read <= 28000000 || (read <= 64000000 && mid < 100)) && tiles_fit(a, 16, 256))
+        EP_LAUNCH_EXPERT(product_small_kernel, max_tiles(M, G, 16) * n_small, 256);
+    a.n_tiles = (int32_t)n_big;
+    if ((per <= 48 || mid <= 384) && mid_fits(a))
+        EP_LAUNCH_EXPERT(product_mid_kernel<false>, mid, kBigThreads);
     return launch_big<false>(a, stream);
 }
 
@@ -754,10 +944,19 @@ extern "C" int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, con
     if (M == 0) return EP_OK;
     a.out_bytes = (int32_t)row_bytes(F, EP_FMT_FP8_E4M3_B128);
     a.n_tiles = F / kScaleBlock;
-    // As above, us: 24 experts, 2176 x 896: 44.9 : 41.0 at 32 rows a group, 48.4 :
-    // 55.7 at 48; 8 experts, 7168 x 1792: 105 : 83 and 111 : 116.
+    // Each kind of tile while few rows leave it no worse filled than the next, or
+    // while its workgroups go round the CUs once or so.  Small : middle : big, us:
+    //   1 row a group      8 experts, 7168 x 1792  63 : 67 : 94   32 of the same 144 : 149 : 200
+    //   16 rows            the same                68 : 80 : 97                  196 : 171 : 226
+    //   32 rows, 24 experts, 2176 x 896            42 : 34 : 45   64 rows 60 : 37 : 48
+    //   256 rows, 1 expert, 7168 x 1792            59 : 77 : 107
+    //   128 rows, 8 experts, 7168 x 1792          (505) : 128 : 126   192 rows 166 : 130
     const int64_t per = ceil_div(M, G);
-    if (per <= 32 && small_fits(a, 1024))
-        EP_LAUNCH_EXPERT(gate_up_small_kernel, max_tiles(M, G, 16) * a.n_tiles, 1024);
+    const int64_t small = max_tiles(M, G, 16) * a.n_tiles;
+    const int64_t mid = max_tiles(M, G, kMidRows) * a.n_tiles;
+    if ((per <= 8 || small <= 352) && tiles_fit(a, 16, 1024))
+        EP_LAUNCH_EXPERT(gate_up_small_kernel, small, 1024);
+    if ((per <= 48 || mid <= 352) && mid_fits(a))
+        EP_LAUNCH_EXPERT(product_mid_kernel<true>, mid, kBigThreads);
     return launch_big<true>(a, stream);
 }
