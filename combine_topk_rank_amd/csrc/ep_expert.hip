@@ -730,6 +730,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_mid_kernel(ExpertArgs 
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int at0 = lane % 16 * 128 + ((lane / 16 ^ (lane % 16 / 2)) * 16), at1 = at0 ^ 64;
     fetch(0);
+    __builtin_amdgcn_sched_barrier(0);   // the meetings count on this order
     fetch(1);
     __builtin_amdgcn_sched_barrier(0);
     scales(0);

@@ -217,6 +217,112 @@ def test_bad_offsets_are_reported(ep):
     assert torch.equal(out[:20], R.grouped64(x, [0, 10, 20, 50], w64)[:20].float().bfloat16())
 
 
+MIXED = [0, 64, 65, 1, 63, 128, 17, 0, 200, 3]
+# Sizes that the middle and the big tiles take: middle ones for 9 to 48 rows a
+# group or few tiles, big ones for more rows and more than 384 (gate: 352) middle
+# tiles.
+LARGER_PRODUCT = [([30] * 20, 1304, 512), (MIXED, 2056, 640), ([9] * 30, 8200, 128), ([40, 1, 0, 7] * 6, 4104, 256),
+                  ([17, 33, 0, 66, 5] * 5, 2600, 384), ([1500], 4104, 128), ([255, 257, 0, 513, 300], 5128, 256),
+                  ([128, 127, 129, 0, 1, 700], 6152, 384), ([40, 1000, 3, 64, 65, 200], 5896, 640)]
+LARGER_GATE_UP = [([30] * 20, 1024, 256), (MIXED, 1280, 384), ([9] * 30, 1024, 128), ([17, 33, 0, 66, 5] * 5, 768, 640),
+                  ([1500], 2048, 128), ([255, 257, 0, 513, 300], 1920, 256), ([128, 127, 129, 0, 1, 700], 2176, 384),
+                  ([40, 1000, 3, 64, 65, 200], 1792, 512)]
+
+
+@pytest.mark.parametrize("counts,N,K", LARGER_PRODUCT)
+def test_larger_product_exact(ep, counts, N, K):
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    off = offsets(counts, 3)
+    M = off[-1] + 7
+    rows, x, w, sw, w64 = exact_inputs(M, len(counts), N, K, gen)
+    log(f"[product] counts={counts[:6]} N={N} K={K}")
+    out, st = product(ep, rows, off, w, sw, M, N)
+    assert st == 0
+    want = R.grouped64(x, off, w64)
+    assert torch.equal(out[3:off[-1]], want[3:off[-1]].float().bfloat16())
+    assert (out[:3] == -7).all() and (out[off[-1]:] == -7).all()
+    # a NaN row and a NaN weight row: nothing else moves
+    bad = min(off[1] if counts[0] else off[2], off[-1] - 1)
+    g = next(i for i, c in enumerate(counts) if c and off[i] <= bad < off[i + 1])
+    rows2, w2 = rows.clone(), w.clone()
+    rows2[bad, K - 1] = 0x7F
+    w2[g, N - 1, 0] = 0xFF
+    dirty, _ = product(ep, rows2, off, w2, sw, M, N)
+    ok = torch.ones_like(out, dtype=torch.bool)
+    ok[bad] = False
+    ok[off[g]:off[g + 1], N - 1] = False
+    assert torch.equal(out[ok], dirty[ok])
+    assert torch.isnan(dirty[bad]).all() and torch.isnan(dirty[off[g]:off[g + 1], N - 1]).all()
+
+
+@pytest.mark.parametrize("counts,F,K", LARGER_GATE_UP)
+def test_larger_gate_up_exact(ep, counts, F, K):
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    off = offsets(counts, 3)
+    M = off[-1] + 7
+    rows, x, w, sw, _ = exact_inputs(M, len(counts), 2 * F, K, gen)
+    sw = sw * 2.0 ** -6
+    w64 = R.weights64(w.view(torch.float8_e4m3fn), sw)
+    log(f"[gate_up] counts={counts[:6]} F={F} K={K}")
+    out, st = gate_up(ep, rows, off, w, sw, M, F)
+    assert st == 0
+    y = R.grouped64(x, off, w64)[3:off[-1]]
+    g, u = y[:, :F], y[:, F:]
+    h = g / (1 + torch.exp(-g)) * u
+    big = g.abs().view(g.shape[0], -1, 128).amax(2)
+    R.assert_rows8(out[3:off[-1]], h, (big + 6) * R.U32, "out_rows")
+    assert (out[:3] == 0xA5).all() and (out[off[-1]:] == 0xA5).all()
+    # a NaN row, and a NaN weight row (the last up): nothing else moves
+    bad = min(off[1] if counts[0] else off[2], off[-1] - 1)
+    e = next(i for i, c in enumerate(counts) if c and off[i] <= bad < off[i + 1])
+    rows2, w2 = rows.clone(), w.clone()
+    rows2[bad, K - 1] = 0x7F
+    w2[e, 2 * F - 1, 0] = 0xFF
+    dirty, _ = gate_up(ep, rows2, off, w2, sw, M, F)
+    ok = torch.ones_like(out, dtype=torch.bool)
+    ok[bad] = False
+    ok[off[e]:off[e + 1], F - 128:F] = False     # the block that shares its scale
+    ok[off[e]:off[e + 1], F + F // 32 - 4:F + F // 32] = False
+    assert torch.equal(out[ok], dirty[ok])
+    assert ((dirty[bad, :F] & 0x7F) == 0x7F).all()
+    assert ((dirty[off[e]:off[e + 1], F - 1] & 0x7F) == 0x7F).all()
+
+
+@pytest.mark.parametrize("counts,N,K", [([40, 30, 25, 0, 50, 8] * 3, 2056, 1792), ([700, 600, 300], 5128, 1792)])
+def test_larger_product_random(ep, counts, N, K):
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    off = offsets(counts)
+    M, G = off[-1], len(counts)
+    rows, x = R.make_rows(torch.randn(M, K, device="cuda", generator=gen) * 3)
+    w, sw, w64 = R.make_weights(G, N, K, gen)
+    out, st = product(ep, rows, off, w, sw, M, N)
+    assert st == 0
+    want = R.grouped64(x, off, w64)
+    R.assert_close(out, want, want.abs() * R.U_BF16 + R.mfma_bound(x, off, w64), "out")
+    assert float((out.double() - want).norm() / want.norm()) <= R.U_BF16 + 2.0 ** -13
+
+
+def test_larger_bad_offsets_are_reported(ep):
+    """Rows beyond M are skipped by the middle and the big tiles too, and
+    offsets out of order write nothing outside the outputs."""
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    for counts, N, K in [([30] * 20, 1304, 512), ([700, 0, 800], 4104, 128)]:
+        off = offsets(counts)
+        M = off[-1]
+        rows, x, w, sw, w64 = exact_inputs(M, len(counts), N, K, gen)
+        guard = torch.full((3 * M, N), -7.0, dtype=torch.bfloat16, device="cuda")
+        st = i32([0])
+        ep.ep_expert_product(rows, i32(off[:-1] + [M + 1]), w, sw, guard[M:2 * M], st)
+        assert int(st) == 3
+        assert torch.equal(guard[M:2 * M], R.grouped64(x, off, w64).float().bfloat16())
+        swapped = list(off)
+        swapped[1], swapped[2] = swapped[2], swapped[1] - 20
+        st = i32([0])
+        ep.ep_expert_product(rows, i32(swapped), w, sw, guard[M:2 * M], st)
+        assert int(st) == 1
+        assert (guard[:M] == -7).all() and (guard[2 * M:] == -7).all()
+
+
 @pytest.mark.parametrize("which", ["product", "gate_up"])
 def test_many_tiles_a_workgroup(ep, which):
     """More tiles than the GPU has CUs, so that workgroups go from one to the
