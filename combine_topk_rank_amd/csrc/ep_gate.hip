@@ -342,12 +342,20 @@ __device__ inline void store_logits(void* p, int64_t base, int sub, int E, const
     }
 }
 
+// Between LDS operations of lanes of one wavefront.
+__device__ inline void lanes_meet() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 template <typename F, int L, int V, bool WIDE>
 __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
     constexpr int kGroups = 256 / L;
     constexpr int kHold = L == 16 ? 2 : 1;     // lane j of a group holds choices j and j + L
     const int sub = (int)threadIdx.x % L;
-    const int group0 = lane_id() & ~(L - 1);
+    // the parts of the group's token that belong to its chosen experts
+    __shared__ __attribute__((aligned(16))) float s_parts[kGroups][L * V];
+    float* const s_place = s_parts[threadIdx.x / L];
     float d[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.0f;
@@ -403,16 +411,26 @@ __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
         // p (d - pd), then each choice's part at its expert
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] *= d[i] - pd;
-        if (a.grad_topk_w)
-            for (int j = 0; j < a.k; ++j) {
-                const bool high = j >= L;
-                const int ej = __shfl(high ? e[kHold - 1] : e[0], group0 + j % L);
-                const float zj = __shfl(high ? z[kHold - 1] : z[0], group0 + j % L);
-                // this lane's register of expert ej, if it has it
-                const int at = ej >= 0 && ej / 4 % L == sub ? ej / (4 * L) * 4 + ej % 4 : -1;
+        if (a.grad_topk_w) {
+            // through the group's LDS: its lanes are of one wavefront, whose LDS
+            // operations run in order, so the fences hold back the compiler only
 #pragma unroll
-                for (int i = 0; i < V; ++i) p[i] += i == at ? zj : 0.0f;
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<f32x4*>(&s_place[expert_of<L>(sub, i)]) =
+                    f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            lanes_meet();
+#pragma unroll
+            for (int q = 0; q < kHold; ++q)
+                if ((uint32_t)e[q] < (uint32_t)a.E) atomicAdd(&s_place[e[q]], z[q]);
+            lanes_meet();
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const f32x4 at = *reinterpret_cast<const f32x4*>(&s_place[expert_of<L>(sub, i)]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) p[i + c] += at[c];
             }
+            lanes_meet();
+        }
         store_logits<F, L, V, WIDE>(a.grad_logits, t * a.E, sub, a.E, p);
     }
 }

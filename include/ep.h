@@ -461,8 +461,8 @@ int ep_route_backward(int32_t T, int32_t E, int32_t k, int32_t dtype, int32_t mo
  *                weight (n,k) is its code times w_scale[n/128, k/128]
  *   out          bf16 [M,N]: out[m,:] = rows[m] times w[g] transposed.  Rows of
  *                no expert are left as they were.
- * K % 128 == 0, K <= 2^20, N % 8 == 0, G <= 4096, M < 2^31; with G = 1 it is a plain
- * matrix product.  Sums are float, blocks of 128 products one matrix
+ * K % 128 == 0, K <= 2^20, 8 <= N <= 2^24, N % 8 == 0, G <= 4096, M < 2^31 (M = 0
+ * launches nothing); with G = 1 it is a plain matrix product.  Sums are float, blocks of 128 products one matrix
  * instruction.  The weights are a serving form: they have no gradient.
  * Device errors: EP_ERR_CAPACITY if an offset exceeds M (rows from M on are
  * skipped), EP_ERR_INVALID_ARG if one is negative or they decrease (outputs
