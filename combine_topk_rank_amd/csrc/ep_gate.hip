@@ -356,16 +356,17 @@ __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
     // the parts of the group's token that belong to its chosen experts
     __shared__ __attribute__((aligned(16))) float s_parts[kGroups][L * V];
     float* const s_place = s_parts[threadIdx.x / L];
-    float d[V];
+    int count[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = 0.0f;
+    for (int i = 0; i < V; ++i) count[i] = 0;
+    float n = 1.0f, grad_loss = 0.0f;
     if (a.grad_balance_loss) {
-        const float n = fmaxf((float)a.num_tokens[0], 1.0f);
-        const float c = a.grad_balance_loss[0] * (float)a.E / n / (n * (float)a.k);
+        n = fmaxf((float)a.num_tokens[0], 1.0f);
+        grad_loss = a.grad_balance_loss[0];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = expert_of<L>(sub, i);
-            if (e < a.E) d[i] = c * (float)a.num_tokens_per_expert[e];
+            if (e < a.E) count[i] = a.num_tokens_per_expert[e];
         }
     }
     for (int64_t t = (int64_t)blockIdx.x * kGroups + (int)threadIdx.x / L; t < a.T;
@@ -396,9 +397,15 @@ __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
         }
         S = group_sum<L>(S);
         const float shift = lse == -__builtin_inff() ? 0.0f : lse;
-        float pd = 0.0f;
+        // d_e here, not ahead of the loop: there it would wait for the counts
+        // before the first logits are asked for
+        float g = grad_loss;
+        asm volatile("" : "+v"(g));
+        const float c = g * (float)a.E / n / (n * (float)a.k);
+        float pd = 0.0f, d[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            d[i] = c * (float)count[i];
             p[i] = expf(p[i] - shift);
             pd = fmaf(p[i], d[i], pd);
         }
