@@ -121,18 +121,21 @@ __global__ __launch_bounds__(STATS ? gate_threads(L * V) : 256) void gate_kernel
     constexpr int kGroups = kThreads / L;
     constexpr int kHold = L == 16 ? 2 : 1;     // lane j of a group holds choices j and j + L
     const int sub = (int)threadIdx.x % L;
-    float sum_p[V];
+    float sum_p[V], v[V];
     int kept = 0;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    int64_t t = (int64_t)blockIdx.x * kGroups + (int)threadIdx.x / L;
+    const auto load = [&]() {
+        if (t < a.T) load_logits<F, L, V, WIDE>(a.logits, t * a.E, sub, a.E, v);
+    };
+    load();    // under way with the mask, ahead of the barrier
     if constexpr (STATS) {
 #pragma unroll
         for (int i = 0; i < V; ++i) sum_p[i] = 0.0f;
         for (int e = (int)threadIdx.x; e < a.E; e += kThreads) s_gate[e] = 0;
         __syncthreads();
     }
-    for (int64_t t = (int64_t)blockIdx.x * kGroups + (int)threadIdx.x / L; t < a.T;
-         t += (int64_t)gridDim.x * kGroups) {
-        float v[V];
-        load_logits<F, L, V, WIDE>(a.logits, t * a.E, sub, a.E, v);   // under way with the mask
+    for (; t < a.T; t += step, load()) {
         if (a.mask && !a.mask[t]) {
             for (int j = sub; j < a.k; j += L) {
                 a.topk_idx[t * a.k + j] = -1;
@@ -217,6 +220,10 @@ __global__ __launch_bounds__(STATS ? gate_threads(L * V) : 256) void gate_kernel
         // the groups of a wavefront, then the wavefronts, in a fixed order
         const int E4 = (a.E + 3) / 4 * 4;
         float* const s_sum = reinterpret_cast<float*>(s_gate + E4);
+        __shared__ int s_kept[kThreads / kWave];
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) kept += __shfl_xor(kept, o);
+        if (lane_id() == 0) s_kept[threadIdx.x / kWave] = kept;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -239,12 +246,12 @@ __global__ __launch_bounds__(STATS ? gate_threads(L * V) : 256) void gate_kernel
             a.part_p[(int64_t)blockIdx.x * a.E + e] = sum;
             a.part_n[(int64_t)blockIdx.x * a.E + e] = s_gate[e];
         }
-        __syncthreads();
-        if (threadIdx.x == 0) s_gate[0] = 0;
-        __syncthreads();
-        if (kept) atomicAdd(&s_gate[0], kept);
-        __syncthreads();
-        if (threadIdx.x == 0) a.part_kept[blockIdx.x] = s_gate[0];
+        if (threadIdx.x == kThreads - 1) {
+            int sum = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / kWave; ++w) sum += s_kept[w];
+            a.part_kept[blockIdx.x] = sum;
+        }
     }
 }
 
