@@ -20,8 +20,10 @@
 //
 // 16384 tokens of 256 experts, k = 8, are 16.8 MB of logits, 3.4 us at a copy's
 // rate; the k rounds cost about 90 instructions for four tokens each, 6 us.
-// With counts and loss: 17 us and 6 of the second kernel; backward 16 us (16
-// lanes a token with one logit a load: 36, 22 and 37 us).
+// With counts and loss: 16 us and 6 of the second kernel (one logit a load: 36 and
+// 22).  Backward: 33 MB, 7 us at a copy's rate, 11 us (37 with one logit a load;
+// 16 while the choices' parts went over all registers in k rounds, 13 while the
+// counts were awaited before the first logits were asked for).
 
 #include "ep_rows8.h"
 
