@@ -37,6 +37,11 @@ struct ExpertArgs {
     int32_t G, N, K, row_bytes, out_bytes, n_tiles;
 };
 
+// Row tiles of bm rows that M rows in G groups can need at most.
+__host__ __device__ inline int64_t max_tiles(int64_t M, int32_t G, int bm) {
+    return M / bm + (G < M ? (int64_t)G : M);
+}
+
 // The rows of a tile of `bm` rows, tiles counted over the groups in order.
 struct RowTile {
     int32_t g;        // group; -1: no such tile
@@ -372,7 +377,10 @@ template <bool GATE>
 __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs a) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[5 * kOperandBytes];
     if (blockIdx.x == 0) check_groups(a);
-    const TileShare share(count_tiles(a.group_offset, a.G, a.M, kBigRows), a.n_tiles);
+    // offsets that decrease can count rows many times: no more than M's tiles
+    const int64_t counted = count_tiles(a.group_offset, a.G, a.M, kBigRows),
+                  most = max_tiles(a.M, a.G, kBigRows);
+    const TileShare share(counted < most ? counted : most, a.n_tiles);
     if (share.count == 0) return;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     // wavefronts 2 wm and 2 wm + 1 share rows: where a tile has few rows, those
@@ -840,11 +848,6 @@ int check_expert(int32_t G, int64_t M, int32_t N, int32_t K) {
     if (K < kScaleBlock || K % kScaleBlock != 0 || K > kMaxK8) return EP_ERR_INVALID_ARG;
     if (N < 8 || N % 8 != 0 || N > kMaxH) return EP_ERR_INVALID_ARG;
     return EP_OK;
-}
-
-// Row tiles of bm rows that M rows in G groups can need at most.
-inline int64_t max_tiles(int64_t M, int32_t G, int bm) {
-    return M / bm + (G < M ? (int64_t)G : M);
 }
 
 }  // namespace ep

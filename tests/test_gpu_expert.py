@@ -323,6 +323,23 @@ def test_larger_bad_offsets_are_reported(ep):
         assert (guard[:M] == -7).all() and (guard[2 * M:] == -7).all()
 
 
+def test_offsets_that_count_rows_many_times(ep):
+    """Offsets that go up and down name more rows than there are: the call
+    reports them, ends, and writes nothing outside its output."""
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    M, G, N, K = 1500, 20, 4104, 128
+    rows, x, w, sw, w64 = exact_inputs(M, G, N, K, gen)
+    guard = torch.full((3 * M, N), -7.0, dtype=torch.bfloat16, device="cuda")
+    for m in (M, 600):     # big tiles, middle tiles
+        st = i32([0])
+        ep.ep_expert_product(rows[:m], i32([0, m] * (G // 2) + [0]), w, sw, guard[M:M + m], st)
+        assert int(st) == 1
+        assert (guard[:M] == -7).all() and (guard[M + M:] == -7).all()
+    guard[M:] = -7.0
+    ep.ep_expert_product(rows[:m], i32([0, m] * (G // 2) + [0]), w, sw, guard[M:M + m], i32([0]))
+    assert (guard[M + m:] == -7).all()
+
+
 @pytest.mark.parametrize("which", ["product", "gate_up"])
 def test_many_tiles_a_workgroup(ep, which):
     """More tiles than the GPU has CUs, so that workgroups go from one to the
