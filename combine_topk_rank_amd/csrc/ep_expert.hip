@@ -654,6 +654,9 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs 
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
+        // the next tile's first two sums take t and these: zero times an infinite
+        // scale of this tile's would be a NaN in another row's
+        sp[0] = sp[1] = 0.0f;
     }
     wait_vm();   // no copy may reach the LDS after the workgroup's end
 }

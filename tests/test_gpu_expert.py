@@ -368,6 +368,48 @@ def test_many_tiles_a_workgroup(ep, which):
         assert st == 0
 
 
+@pytest.mark.parametrize("which", ["product", "gate_up"])
+@pytest.mark.parametrize("counts,N,K", [([20, 70, 3], 256, 256), ([30] * 20, 2048, 512),
+                                        ([1000, 0, 256, 3, 2817, 511], 5888, 256)])
+def test_infinite_scales_stay_in_their_rows(ep, which, counts, N, K):
+    """An infinite scale in the last block of K of some rows, or of one expert's
+    weights, changes no other row, in small, middle and big tiles; of the last
+    there are more than CUs, so that a workgroup goes from a tile with such a
+    scale to one without."""
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    off = offsets(counts, 2)
+    M, G = off[-1] + 5, len(counts)
+    rows, x, w, sw, _ = exact_inputs(M, G, N, K, gen)
+    f, n = (product, N) if which == "product" else (gate_up, N // 2)
+    log(f"[infinite scales] {which} counts={counts[:6]} N={N} K={K}")
+    clean, st = f(ep, rows, off, w, sw, M, n)
+    assert st == 0
+    place = torch.full((M,), -1, device="cuda")
+    for g in range(G):
+        place[off[g]:off[g + 1]] = torch.arange(counts[g], device="cuda")
+    # of every third 256 rows of an expert, the second half of each 64
+    bad = (place >= 0) & (place // 256 % 3 == 0) & (place % 64 >= 32) if max(counts) >= 64 else place == 29
+    assert bad.any()
+    rows2 = rows.clone()
+    inf = torch.full((1,), float("inf"), device="cuda").view(torch.uint8)
+    rows2[bad, K + K // 32 - 4:K + K // 32] = inf
+    dirty, st = f(ep, rows2, off, w, sw, M, n)
+    assert st == 0
+    assert torch.equal(clean[~bad].view(torch.uint8), dirty[~bad].view(torch.uint8))
+    if which == "product":
+        assert not torch.isfinite(dirty[bad]).any()
+    for g in range(min(G, 6)):
+        sw2 = sw.clone()
+        sw2[g, :, -1] = float("inf")
+        dirty, st = f(ep, rows, off, w, sw2, M, n)
+        assert st == 0
+        other = torch.ones(M, dtype=torch.bool, device="cuda")
+        other[off[g]:off[g + 1]] = False
+        assert torch.equal(clean[other].view(torch.uint8), dirty[other].view(torch.uint8)), f"expert {g}"
+        if which == "product":
+            assert not torch.isfinite(dirty[~other]).any()
+
+
 def test_weights_as_float8_and_many_groups(ep):
     """1024 experts, most without rows; codes passed as float8."""
     gen = torch.Generator(device="cuda").manual_seed(7)
