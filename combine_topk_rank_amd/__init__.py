@@ -771,8 +771,14 @@ class BuffersMoE(BuffersLL):
         self.y = torch.empty((cap, H), **bf)
 
     def norm(self, x, residual, weight, eps, stream=None):
-        """self.residual = x + residual and self.normed, its norm"""
-        ep_rmsnorm(x, residual, weight, eps, self.residual, self.normed, None, self.rstd, stream)
+        """self.residual = x + residual (x where residual is None, a first
+        layer's) and self.normed, its norm"""
+        ep_rmsnorm(x, residual, weight, eps, None if residual is None else self.residual,
+                   self.normed, None, self.rstd, stream)
+        if residual is None:    # the call has no residual sum to store then
+            import torch
+            with torch.cuda.stream(stream):
+                self.residual.copy_(x)
 
     def route(self, logits, mode=EP_GATE_SOFTMAX_RENORM, token_mask=None, stream=None):
         ep_route(logits, token_mask, mode, self.topk_idx, self.topk_w, stream=stream)

@@ -157,3 +157,62 @@ def test_two_steps_at_once_on_two_streams(ep):
         torch.cuda.synchronize()
         for (buf, _, _), w in zip(sets, want):
             assert torch.equal(buf.out, w)
+
+
+@pytest.mark.parametrize("T", [0, 1, 130])
+def test_block_without_a_residual(ep, T):
+    """A first layer has no residual: the residual stream begins as x."""
+    H, E, k, F = 512, 16, 4, 256
+    d = make(T, H, E, F, 6)
+    d["residual"] = None
+    buf = ep.BuffersMoE(ep.shape(T, H, E, 4, k, ep.EP_FMT_FP8_E4M3_B128), F)
+    buf.residual.fill_(-7.0)
+    out = buf.block(d["x"], None, d["weight"], EPS, lambda n: n.float() @ d["router"].t(), d["w1"], d["s1"], d["w2"],
+                    d["s2"])
+    assert int(buf.dev_status) == 0
+    assert out.shape == (T, H) and torch.equal(buf.residual, d["x"])
+    if T:
+        _, want = reference(d, buf.topk_idx, buf.topk_w)
+        assert float((out.double() - want).norm() / want.norm()) <= 2.0 ** -6
+    # the residual stream itself as x, as where the caller has put it there
+    again = out.clone()
+    assert torch.equal(buf.block(buf.residual, None, d["weight"], EPS, lambda n: n.float() @ d["router"].t(), d["w1"],
+                                 d["s1"], d["w2"], d["s2"]), again)
+    assert torch.equal(buf.residual, d["x"])
+    with pytest.raises(ValueError, match="x must"):      # and nothing is copied from a refused x
+        buf.norm(d["x"].float(), None, d["weight"], EPS)
+    assert torch.equal(buf.residual, d["x"])
+
+
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_block_in_a_graph_and_on_a_stream(ep, with_residual):
+    T, H, E, k, F = 96, 512, 16, 4, 256
+    d = make(T, H, E, F, 7)
+    residual = d["residual"] if with_residual else None
+    buf = ep.BuffersMoE(ep.shape(T, H, E, 4, k, ep.EP_FMT_FP8_E4M3_B128), F)
+    run = lambda: buf.block(d["x"], residual, d["weight"], EPS, lambda n: n.float() @ d["router"].t(),  # noqa: E731
+                            d["w1"], d["s1"], d["w2"], d["s2"])
+    run()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        run()
+    for seed in range(3):
+        d["x"].copy_(make(T, H, E, F, 20 + seed)["x"])
+        run()
+        torch.cuda.synchronize()
+        out, r = buf.out.clone(), buf.residual.clone()
+        buf.out.fill_(float("nan"))
+        buf.residual.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(buf.out, out) and torch.equal(buf.residual, r)
+    # the norm on a stream that is not the current one
+    buf.residual.fill_(float("nan"))
+    buf.normed.fill_(float("nan"))
+    torch.cuda.synchronize()
+    buf.norm(d["x"], residual, d["weight"], EPS, stream=s)
+    s.synchronize()
+    assert torch.equal(buf.residual, r) and torch.isfinite(buf.normed).all()
