@@ -411,14 +411,20 @@ __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
         float g = grad_loss;
         asm volatile("" : "+v"(g));
         const float c = g * (float)a.E / n / (n * (float)a.k);
-        float pd = 0.0f, d[V];
+        float pd = 0.0f, total = 0.0f, d[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             d[i] = c * (float)count[i];
             p[i] = expf(p[i] - shift);
+            total += p[i];
             pd = fmaf(p[i], d[i], pd);
         }
-        pd = group_sum<L>(pd);
+        // lse is a float: far from zero it is off by more than p may be (by log E
+        // where the logits are the type's lowest value), alike for all of the
+        // token's p, so their sum, one but for that, takes it out
+        total = group_sum<L>(total);
+        const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+        pd = group_sum<L>(pd) * inv;
         if (a.renorm)
 #pragma unroll
             for (int q = 0; q < kHold; ++q) z[q] = fmaf(-w[q], S, z[q]);
@@ -426,7 +432,7 @@ __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
             pd += S;
         // p (d - pd), then each choice's part at its expert
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] *= d[i] - pd;
+        for (int i = 0; i < V; ++i) p[i] *= inv * (d[i] - pd);
         if (a.grad_topk_w) {
             // through the group's LDS: its lanes are of one wavefront, whose LDS
             // operations run in order, so the fences hold back the compiler only

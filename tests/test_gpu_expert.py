@@ -429,6 +429,28 @@ def test_weights_as_float8_and_many_groups(ep):
     assert st == 0 and (out[off[-1]:] == 0xA5).all() and not (out[:off[-1], N + 4:] != 0).any()
 
 
+@pytest.mark.parametrize("float8", [False, True])
+def test_gate_up_of_many_groups(ep, float8):
+    """1024 experts, most without rows, all with weights of their own: values."""
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    G, F, K = 1024, 128, 128
+    r = np.random.RandomState(15)
+    counts = np.bincount(r.randint(0, G, 400), minlength=G)
+    off = offsets(counts)
+    M = off[-1] + 3
+    rows, x, w, sw, _ = exact_inputs(M, G, 2 * F, K, gen)
+    sw = sw * 2.0 ** -6
+    w64 = R.weights64(w.view(torch.float8_e4m3fn), sw)
+    out, st = gate_up(ep, rows, off, w.view(torch.float8_e4m3fn) if float8 else w, sw, M, F)
+    y = R.grouped64(x, off, w64)[:off[-1]]
+    g, u = y[:, :F], y[:, F:]
+    h = g / (1 + torch.exp(-g)) * u
+    big = g.abs().view(g.shape[0], -1, 128).amax(2)
+    assert st == 0
+    R.assert_rows8(out[:off[-1]], h, (big + 6) * R.U32, "out_rows")
+    assert (out[off[-1]:] == 0xA5).all()
+
+
 def test_same_bits_each_time_and_graph(ep):
     gen = torch.Generator(device="cuda").manual_seed(9)
     counts, H, F = [0, 12, 200, 7], 512, 256

@@ -191,6 +191,48 @@ def test_backward(ep, T, E, k, half, mode, masked, parts):
     check_back(backward(ep, logits, mask, mode, o, gw, gl), logits, mask, k, mode, gw, gl)
 
 
+@pytest.mark.parametrize("T,E,k", [(40, 20, 3), (33, 256, 8), (9, 777, 9)])
+@pytest.mark.parametrize("mode", [0, 1])
+def test_backward_far_from_zero(ep, T, E, k, mode):
+    """Softmax does not change when a token's logits move together: logits of
+    whole 256ths around 8192, held exactly, have the gradients of those around
+    0, within the tolerance of those (lse, held in float, is itself off by up to
+    2^-11 there)."""
+    logits, _ = make(T, E, False, 19)
+    logits = (logits * 256).round() / 256
+    far = logits + 8192.0
+    assert torch.equal(far - 8192.0, logits)
+    o = forward(ep, far, None, k, mode)
+    g = torch.Generator(device="cuda").manual_seed(20)
+    gw, gl = torch.randn(T, k, device="cuda", generator=g), torch.full((1,), 0.3, device="cuda")
+    assert torch.equal(o["topk_idx"], R.route64(logits, keep_of(logits, None), k, mode)[0])
+    check_back(backward(ep, far, None, mode, o, gw, gl), logits, None, k, mode, gw, gl)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("E,k", [(12, 3), (256, 8), (300, 5)])
+def test_rows_of_the_lowest_value(ep, E, k, half, mode):
+    """A token whose logits are all the type's lowest value, or all but some
+    that are -inf, has equal probabilities, as with logits of zero."""
+    kind = torch.bfloat16 if half else torch.float32
+    T = 5
+    logits, _ = make(T, E, half, 21)
+    logits[1:4] = torch.finfo(kind).min
+    logits[2, 1::2] = float("-inf")
+    zero = logits.clone()
+    zero[1:4] = 0.0
+    zero[2, 1::2] = float("-inf")
+    o = forward(ep, logits, None, k, mode)
+    same = forward(ep, zero, None, k, mode)
+    for n in ("topk_idx", "topk_w", "num_tokens_per_expert", "balance_loss"):
+        assert torch.equal(o[n], same[n]), n
+    gw, gl = torch.ones(T, k, device="cuda"), torch.full((1,), 0.3, device="cuda")
+    gw[:, 0] = -2.0
+    near = zero.clamp_min(-200.0)     # exp(-200) is no more than -inf's in float, and a finite span
+    check_back(backward(ep, logits, None, mode, o, gw, gl), near, None, k, mode, gw, gl)
+
+
 def test_backward_in_place(ep):
     logits, mask = make(200, 48, False, 8, True)
     keep = logits.clone()

@@ -216,3 +216,15 @@ def test_block_in_a_graph_and_on_a_stream(ep, with_residual):
     buf.norm(d["x"], residual, d["weight"], EPS, stream=s)
     s.synchronize()
     assert torch.equal(buf.residual, r) and torch.isfinite(buf.normed).all()
+
+
+def test_block_of_padded_tokens_alone(ep):
+    """No expert has a row: the output is zero, the residual stream goes on."""
+    T, H, E, k, F = 20, 256, 8, 2, 128
+    d = make(T, H, E, F, 8)
+    buf = ep.BuffersMoE(ep.shape(T, H, E, 2, k, ep.EP_FMT_FP8_E4M3_B128), F)
+    out = buf.block(d["x"], d["residual"], d["weight"], EPS, lambda n: n.float() @ d["router"].t(), d["w1"], d["s1"],
+                    d["w2"], d["s2"], token_mask=torch.zeros(T, dtype=torch.uint8, device="cuda"))
+    assert int(buf.dev_status) == 0 and int(buf.expert_offset.abs().max()) == 0
+    assert (out == 0).all()
+    assert torch.equal(buf.residual, R.norm64(d["x"], d["residual"], d["weight"], EPS)[0])
