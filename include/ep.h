@@ -383,8 +383,10 @@ int ep_combine_ll(const ep_shape_t* shape, const void* y, int64_t y_rows,
  *                 (quantised from float, not from the bf16 y), or NULL;
  *                 needs H % 128 == 0.  One of y and rows at least.
  *   rstd          float [T]: rsqrt(mean(r^2) + eps), for the backward, or NULL
- * The sum of squares is float: it overflows for values beyond about 1e19 (y is
- * then 0), and with eps = 0 a row of zeros gives NaN.
+ * The sum of squares is float: it overflows for a root mean square beyond
+ * 1.8e19 / sqrt(H) (y is then 0).  With eps = 0 a row of zeros gives NaN; rows
+ * whose root mean square is below 1e-18 lose digits, and where every value is
+ * below 2^-75 y is infinite (NaN for zeros).
  * 8 <= H <= 32768, H % 8 == 0; eps >= 0 and finite.  residual_out or y may be
  * x or residual themselves (a row is read before it is written), but not the
  * same one.  Every pointer 16-byte aligned, rstd 4-byte. */

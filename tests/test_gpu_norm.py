@@ -106,6 +106,23 @@ def test_values_that_are_not_ordinary(ep):
         torch.allclose(scales[3:5], torch.full_like(scales[3:5], 1e-4 / 448.0), rtol=1e-6)
 
 
+@pytest.mark.parametrize("H", [512, 7168])
+def test_limits_of_the_sum_of_squares(ep, H):
+    """Rows at the ends of what the header states: up to a root mean square of
+    1.8e19 / sqrt(H) they are normalised, beyond it y is 0; with eps = 0 down to
+    1e-18, and below 2^-75 rstd is infinite."""
+    _, _, w, f = make(5, H, 6)
+    sign = torch.where(f(5, H) < 0, -1.0, 1.0)
+    size = torch.tensor([1.7e19 / H ** 0.5, 1.9e19 / H ** 0.5, 1e-18, 2.0 ** -76, 1.0], device="cuda")
+    x = (sign * size[:, None]).bfloat16()
+    o = outputs(ep, 5, H, residual=False)
+    ep.ep_rmsnorm(x, None, w, 0.0, **o)
+    good = [0, 2, 4]
+    check({k: None if v is None else v[good] for k, v in o.items()}, x[good], None, w, 0.0)
+    assert o["rstd"][1] == 0 and (o["y"][1] == 0).all()
+    assert torch.isinf(o["rstd"][3]) and torch.isinf(o["y"][3]).all()
+
+
 def test_overflowing_elements_take_the_dispatch_codes(ep):
     """A weight that makes y infinite: the block's scale is infinite, its finite
     elements are zero and the infinite one is the NaN code with its sign, as
