@@ -451,6 +451,34 @@ def test_gate_up_of_many_groups(ep, float8):
     assert (out[off[-1]:] == 0xA5).all()
 
 
+@pytest.mark.parametrize("which", ["product", "gate_up"])
+@pytest.mark.parametrize("each,N,K", [(12, 520, 128), (70, 1024, 256)])
+def test_more_than_64_groups_of_larger_tiles(ep, which, each, N, K):
+    """Middle and big tiles whose groups take a wavefront several looks: 200
+    experts, every third without rows, the last with many."""
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    counts = [0 if g % 3 == 1 else each + g % 29 for g in range(199)] + [900]
+    off = offsets(counts, 1)
+    M, n = off[-1] + 2, N if which == "product" else 512
+    rows, x, w, sw, _ = exact_inputs(M, 200, n if which == "product" else 2 * n, K, gen)
+    inside = slice(1, off[-1])
+    if which == "product":
+        out, st = product(ep, rows, off, w, sw, M, n)
+        want = R.grouped64(x, off, R.weights64(w.view(torch.float8_e4m3fn), sw))
+        assert torch.equal(out[inside], want[inside].float().bfloat16())
+        assert (out[:1] == -7).all() and (out[off[-1]:] == -7).all()
+    else:
+        sw = sw * 2.0 ** -6
+        out, st = gate_up(ep, rows, off, w, sw, M, n)
+        y = R.grouped64(x, off, R.weights64(w.view(torch.float8_e4m3fn), sw))[inside]
+        g, u = y[:, :n], y[:, n:]
+        h = g / (1 + torch.exp(-g)) * u
+        big = g.abs().view(g.shape[0], -1, 128).amax(2)
+        R.assert_rows8(out[inside], h, (big + 6) * R.U32, "out_rows")
+        assert (out[:1] == 0xA5).all() and (out[off[-1]:] == 0xA5).all()
+    assert st == 0
+
+
 def test_same_bits_each_time_and_graph(ep):
     gen = torch.Generator(device="cuda").manual_seed(9)
     counts, H, F = [0, 12, 200, 7], 512, 256
