@@ -752,7 +752,11 @@ class BuffersLL(Buffers):
 class BuffersMoE(BuffersLL):
     """Buffers of a whole mixture-of-experts block over per-expert rows in 8
     bits (``s.fmt`` EP_FMT_FP8_E4M3_B128): norm, router, dispatch, the experts'
-    two products of inner width ``F`` and combine, in this order."""
+    two products of inner width ``F`` and combine, in this order.
+
+    A serving form: ``route`` makes the choices and their gates alone.  The counts,
+    the balance loss and the lse that ep_route_backward takes come from ep_route
+    with a workspace."""
 
     def __init__(self, s: ep_shape_t, F: int, capacity_rows: Optional[int] = None, device="cuda"):
         import torch

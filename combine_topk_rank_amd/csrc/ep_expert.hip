@@ -175,13 +175,15 @@ __device__ inline void store_block(const ExpertArgs& a, int64_t m, int fb, const
 
 // Few rows a group, with the gate: a workgroup has the 128 gates and 128 ups
 // of one output block and 16 rows; wavefront w has 16 of those weight rows over
-// all of K.  Weights go from memory to registers, a block ahead; the 16
-// wavefronts share the rows through LDS, sixteen blocks at a time and the next
-// sixteen under way, since a CU takes in no more than about 25 GB/s: with rows
-// read once a wavefront, 4 rows at each of 8 experts, 7168 x 1792, took 118 us
-// and one row 73.  Now 66 and 65 (3.2 TB/s: 112 of the 256 CUs have work); 24
-// experts of 2176 x 896 take 20 us (4.6 TB/s).  One block ahead, two workgroups
-// a CU: with two or four ahead, and fewer wavefronts, 25 and 32 us.
+// all of K.  Weights go from memory to registers, one block under way while the
+// one before is multiplied; the 16 wavefronts share the rows through LDS, sixteen
+// blocks at a time and the next sixteen under way: with rows read once a
+// wavefront, 4 rows at each of 8 experts, 7168 x 1792, took 118 us and one row
+// 73.  Now 66 and 65 (3.2 TB/s over the 112 CUs that have work, 28 GB/s each);
+// 24 experts of 2176 x 896 take 20 us (4.7 TB/s over 168 workgroups, 28 GB/s each).
+// Bound by the round trip to memory, one a block of K: 56 of them at K = 7168.
+// For the many rounds of more groups, two workgroups a CU and one block ahead:
+// with two or four ahead, and fewer wavefronts, the 20 us became 25 and 32.
 constexpr int kSlab = 16;                              // blocks of K of the rows in LDS
 constexpr int kSlabPitch = kSlab * kScaleBlock + 16;   // 16 rows' reads meet all banks once
 
@@ -664,13 +666,17 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs 
 // ---- Some rows a group ----------------------------------------------------------
 // 256 weight rows x up to 64 rows a workgroup: a wavefront has 32 of the weight
 // rows (for the gate: 16 gates and their ups) and all the rows.  Four blocks of
-// K of both operands, 40 KB each, fill the LDS, three of them under way.
+// K of both operands, 40 KB each, fill the LDS: one in use, two under way behind
+// it, and one whose copies follow.  (The wait for a block's scales, asked for
+// between the copies of the next two blocks, is a wait for the first of these too:
+// memory operations end in their order.)
 // Between the others in both respects: a weight row is read once for 64 rows where
 // the small tiles read it four times, and four times as many workgroups share the
-// work as with the big tiles.  Bound by memory and the copies' latency: the gate of
-// 24 experts of 2176 x 896 with 60 rows each (94 MB of weights) 38 us where big
-// tiles take 53; the product of 32 experts of 7168 x 1792 with 4 rows each (411 MB)
-// 66-79 us, 5.2-6.2 TB/s.
+// work as with the big tiles.  Bound by the copies' latency for middling groups:
+// the gate of 24 experts of 2176 x 896 with 60 rows each (94 MB of weights, 19 us
+// at a copy's rate) 38 us where big tiles take 53.  Bound by memory for few rows:
+// the product of 120 rows over 32 experts of 7168 x 1792, of which about 27 have
+// rows (342 MB), 66-79 us, 4.3-5.2 TB/s.
 constexpr int kMidRows = 64;
 constexpr int kMidStages = 4;
 constexpr int kMidBytes = kOperandBytes + kMidRows * kScaleBlock;
@@ -755,7 +761,8 @@ __global__ __launch_bounds__(kBigThreads, 2) void product_mid_kernel(ExpertArgs 
     fetch(2);
     for (int b = 0; b < nb; ++b) {
         // block b is here when all but the two copies behind it and the scales
-        // between them are; everyone is then done with block b - 1
+        // between them are; everyone is then done with block b - 1.  The scales'
+        // first use waits for them, and so for block b + 1.
         meet<5 + 4 + kHalves + 5, 0>();
         float s[2][4];
 #pragma unroll
@@ -933,6 +940,8 @@ extern "C" int ep_expert_product(int32_t G, int64_t M, int32_t N, int32_t K, con
     //   8 rows, 32 experts, 1024 x 512 (25 MB)    8.4 : 10 : 12   48 rows 18 : 12 : 18
     //   64 rows, 1 expert, 7168 x 1792 (56 tiles)  17 : 22 : 22   128 rows 31 : 23 : 26
     //   96 rows, 8 experts, 7168 x 1792 (560)     126 : 48 : 39   24 of 2176 x 896 62 : 29 : 24
+    // (64 rows of one expert are counted as five tiles, 64.2 million bytes, and take
+    // middle ones: 25 us with weights that no cache holds)
     const int64_t per = ceil_div(M, G);   // rows a group, were they even
     const int64_t n_small = ceil_div(N, 16), n_big = ceil_div(N, kBigRows);
     const int64_t read = max_tiles(M, G, 16) * N * K, mid = max_tiles(M, G, kMidRows) * n_big;
