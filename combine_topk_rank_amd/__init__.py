@@ -33,8 +33,21 @@ The functions keep the C names:
                       num_tokens, lse, grad_topk_w, grad_balance_loss, grad_logits, stream=None)
     ep_expert_product(rows, group_offset, w, w_scale, out, dev_status, stream=None)
     ep_expert_gate_up(rows, group_offset, w, w_scale, out_rows, dev_status, stream=None)
-        (these six take their sizes from the tensors and check every one: a wrong type,
-        shape, device or stride raises ValueError)
+    ep_combine_backward(shape, y, topk_idx, topk_w, send_slot, grad_out, grad_y, grad_topk_w,
+                        dev_status, stream=None)             # ep_combine_ll_backward: expert_slot
+    ep_dispatch_backward(shape, topk_idx, send_slot, grad_rows, grad_slot_local_w, grad_other,
+                         grad_x, grad_topk_w, dev_status, stream=None)
+        (ep_dispatch_ll_backward: expert_slot and grad_slot_w)
+    ep_expert_product_bf16(rows, group_offset, w, out, dev_status, stream=None)
+    ep_expert_product_bf16_backward(rows, group_offset, w, grad_out, grad_rows, grad_w, dev_status,
+                                    workspace=None, stream=None)
+    ep_expert_gate_up_bf16(rows, group_offset, w, pre, out, dev_status, stream=None)
+    ep_expert_gate_up_bf16_backward(rows, group_offset, w, pre, grad_out, grad_pre, grad_rows,
+                                    grad_w, dev_status, workspace=None, stream=None)
+    ep_grad_norm(tensors, sum_squares, norm, workspace, stream=None)
+    ep_grad_clip(tensors, sum_squares, max_norm, into=None, stream=None)
+        (these take their sizes from the tensors, or check them against the shape: a wrong
+        type, shape, device or stride raises ValueError)
     Ring(depth, channels, max_inflight, timeout_ns)   # ep_ring_* calls
 
 Tensors are torch tensors on the current HIP device (contiguous); ``stream``
@@ -88,6 +101,11 @@ class EpError(RuntimeError):
         if status == EP_ERR_HIP:
             detail = " [" + lib.ep_last_error().decode() + "]"
         super().__init__(f"{where}: {status_str(status)} ({status}){detail}")
+
+
+class ep_tensor_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("pad_", ctypes.c_int32)]
 
 
 class ep_shape_t(ctypes.Structure):
@@ -152,6 +170,32 @@ def _load() -> ctypes.CDLL:
     L.ep_expert_product.restype = ctypes.c_int
     L.ep_expert_gate_up.argtypes = [i32, i64, i32, i32, P, P, P, P, P, P, P]
     L.ep_expert_gate_up.restype = ctypes.c_int
+    L.ep_combine_backward.argtypes = [S, P, i64, P, P, P, P, P, P, P, P]
+    L.ep_combine_backward.restype = ctypes.c_int
+    L.ep_combine_ll_backward.argtypes = L.ep_combine_backward.argtypes
+    L.ep_combine_ll_backward.restype = ctypes.c_int
+    L.ep_dispatch_backward.argtypes = [S, P, P, P, i64, P, P, P, P, P, P]
+    L.ep_dispatch_backward.restype = ctypes.c_int
+    L.ep_dispatch_ll_backward.argtypes = L.ep_dispatch_backward.argtypes
+    L.ep_dispatch_ll_backward.restype = ctypes.c_int
+    L.ep_expert_product_bf16.argtypes = [i32, i64, i32, i32, P, P, P, P, P, P]
+    L.ep_expert_product_bf16.restype = ctypes.c_int
+    L.ep_expert_gate_up_bf16.argtypes = [i32, i64, i32, i32, P, P, P, P, P, P, P]
+    L.ep_expert_gate_up_bf16.restype = ctypes.c_int
+    L.ep_expert_backward_workspace_bytes.argtypes = [i32, i64, i32, i32]
+    L.ep_expert_backward_workspace_bytes.restype = sz
+    L.ep_expert_product_bf16_backward.argtypes = [i32, i64, i32, i32, i32, P, P, P, P, P, P, P, P,
+                                                  sz, P]
+    L.ep_expert_product_bf16_backward.restype = ctypes.c_int
+    L.ep_expert_gate_up_bf16_backward.argtypes = [i32, i64, i32, i32, i32, P, P, P, P, P, P, P, P,
+                                                  P, P, sz, P]
+    L.ep_expert_gate_up_bf16_backward.restype = ctypes.c_int
+    L.ep_grad_norm_workspace_bytes.argtypes = [i32]
+    L.ep_grad_norm_workspace_bytes.restype = sz
+    L.ep_grad_norm.argtypes = [i32, P, P, P, P, sz, P]
+    L.ep_grad_norm.restype = ctypes.c_int
+    L.ep_grad_clip.argtypes = [i32, P, P, P, ctypes.c_double, P]
+    L.ep_grad_clip.restype = ctypes.c_int
     L.ep_ring_create.argtypes = [i32, i32, i32, i64]
     L.ep_ring_create.restype = P
     L.ep_ring_destroy.argtypes = [P]
@@ -551,6 +595,257 @@ def ep_expert_gate_up(rows, group_offset, w, w_scale, out_rows, dev_status, stre
     _check(st, "ep_expert_gate_up")
 
 
+def _slots(s, name, slot, topk_idx, device, ll):
+    """Addresses of topk_idx and of the layout's slots, [T, R] or, per expert, [T, k]."""
+    return (_arg("topk_idx", _need("topk_idx", topk_idx), _I32, (s.T, s.k), device),
+            _arg(name, _need(name, slot), _I32, (s.T, s.k if ll else s.R), device))
+
+
+def _status(dev_status, device):
+    return _arg("dev_status", _need("dev_status", dev_status), _I32, (1,), device)
+
+
+def _rows_of(s, name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, H]")
+    return t.shape[0]
+
+
+def _combine_backward(call, where, ll, s, y, topk_idx, topk_w, slot_name, slot, grad_out, grad_y,
+                      grad_topk_w, dev_status, stream) -> None:
+    device, st_ = _call_device(stream)
+    if grad_y is None and grad_topk_w is None:
+        raise ValueError("one of grad_y and grad_topk_w must be given")
+    if grad_topk_w is not None:
+        _need("y", y)
+    rows = _rows_of(s, "y", y) if y is not None else _rows_of(s, "grad_y", grad_y)
+    idx, slots = _slots(s, slot_name, slot, topk_idx, device, ll)
+    st = call(ctypes.byref(s), _arg("y", y, _BF16, (rows, s.H), device), rows, idx,
+              _arg("topk_w", _need("topk_w", topk_w), _F32, (s.T, s.k), device), slots,
+              _arg("grad_out", _need("grad_out", grad_out), _BF16, (s.T, s.H), device),
+              _arg("grad_y", grad_y, _BF16, (rows, s.H), device),
+              _arg("grad_topk_w", grad_topk_w, _F32, (s.T, s.k), device),
+              _status(dev_status, device), st_)
+    _check(st, where)
+
+
+def ep_combine_backward(s, y, topk_idx, topk_w, send_slot, grad_out, grad_y, grad_topk_w,
+                        dev_status, stream=None) -> None:
+    _combine_backward(lib.ep_combine_backward, "ep_combine_backward", False, s, y, topk_idx, topk_w,
+                      "send_slot", send_slot, grad_out, grad_y, grad_topk_w, dev_status, stream)
+
+
+def ep_combine_ll_backward(s, y, topk_idx, topk_w, expert_slot, grad_out, grad_y, grad_topk_w,
+                           dev_status, stream=None) -> None:
+    _combine_backward(lib.ep_combine_ll_backward, "ep_combine_ll_backward", True, s, y, topk_idx,
+                      topk_w, "expert_slot", expert_slot, grad_out, grad_y, grad_topk_w, dev_status,
+                      stream)
+
+
+def _dispatch_backward(call, where, ll, s, topk_idx, slot_name, slot, grad_rows, gates_name, gates,
+                       grad_other, grad_x, grad_topk_w, dev_status, stream) -> None:
+    device, st_ = _call_device(stream)
+    rows = _rows_of(s, "grad_rows", _need("grad_rows", grad_rows))
+    if (gates is None) != (grad_topk_w is None):
+        raise ValueError(f"{gates_name} and grad_topk_w belong together")
+    idx, slots = _slots(s, slot_name, slot, topk_idx, device, ll)
+    st = call(ctypes.byref(s), idx, slots, _arg("grad_rows", grad_rows, _BF16, (rows, s.H), device),
+              rows, _arg(gates_name, gates, _F32, (rows,) if ll else (rows, s.k), device),
+              _arg("grad_other", grad_other, _BF16, (s.T, s.H), device),
+              _arg("grad_x", _need("grad_x", grad_x), _BF16, (s.T, s.H), device),
+              _arg("grad_topk_w", grad_topk_w, _F32, (s.T, s.k), device),
+              _status(dev_status, device), st_)
+    _check(st, where)
+
+
+def ep_dispatch_backward(s, topk_idx, send_slot, grad_rows, grad_slot_local_w, grad_other, grad_x,
+                         grad_topk_w, dev_status, stream=None) -> None:
+    _dispatch_backward(lib.ep_dispatch_backward, "ep_dispatch_backward", False, s, topk_idx,
+                       "send_slot", send_slot, grad_rows, "grad_slot_local_w", grad_slot_local_w,
+                       grad_other, grad_x, grad_topk_w, dev_status, stream)
+
+
+def ep_dispatch_ll_backward(s, topk_idx, expert_slot, grad_rows, grad_slot_w, grad_other, grad_x,
+                            grad_topk_w, dev_status, stream=None) -> None:
+    _dispatch_backward(lib.ep_dispatch_ll_backward, "ep_dispatch_ll_backward", True, s, topk_idx,
+                       "expert_slot", expert_slot, grad_rows, "grad_slot_w", grad_slot_w,
+                       grad_other, grad_x, grad_topk_w, dev_status, stream)
+
+
+def _bf16_args(rows, group_offset, w, device, weights=None, width=None):
+    """G, M, weight rows, K and the addresses of rows, offsets and w.  In a backward
+    rows or w may be None: the sizes then come from grad_w (`weights`) or grad_out."""
+    sized = w if w is not None else _need("w", weights)
+    if sized.dim() != 3:
+        raise ValueError("w must be [G, N, K]")
+    G, N, K = sized.shape
+    if rows is None and width is None:
+        _need("rows", rows)
+    M = rows.shape[0] if rows is not None else width.shape[0]
+    return (G, M, N, K, _arg("rows", rows, _BF16, (M, K), device),
+            _arg("group_offset", _need("group_offset", group_offset), _I32, (G + 1,), device),
+            _arg("w", w, _BF16, (G, N, K), device))
+
+
+def ep_expert_product_bf16(rows, group_offset, w, out, dev_status, stream=None) -> None:
+    device, st_ = _call_device(stream)
+    G, M, N, K, *inputs = _bf16_args(_need("rows", rows), group_offset, _need("w", w), device)
+    st = lib.ep_expert_product_bf16(G, M, N, K, *inputs,
+                                    _arg("out", _need("out", out), _BF16, (M, N), device),
+                                    _status(dev_status, device), st_)
+    _check(st, "ep_expert_product_bf16")
+
+
+def ep_expert_gate_up_bf16(rows, group_offset, w, pre, out, dev_status, stream=None) -> None:
+    device, st_ = _call_device(stream)
+    G, M, N, K, *inputs = _bf16_args(_need("rows", rows), group_offset, _need("w", w), device)
+    if N % 16:
+        raise EpError(EP_ERR_INVALID_ARG, "ep_expert_gate_up_bf16")
+    st = lib.ep_expert_gate_up_bf16(G, M, N // 2, K, *inputs,
+                                    _arg("pre", pre, _BF16, (M, N), device),
+                                    _arg("out", _need("out", out), _BF16, (M, N // 2), device),
+                                    _status(dev_status, device), st_)
+    _check(st, "ep_expert_gate_up_bf16")
+
+
+def ep_expert_backward_workspace_bytes(G: int, M: int, N: int, K: int) -> int:
+    return int(lib.ep_expert_backward_workspace_bytes(G, M, N, K))
+
+
+def _weights_type(grad_w) -> int:
+    if grad_w is None or grad_w.dtype is _BF16:
+        return EP_BF16
+    if grad_w.dtype is _F32:
+        return EP_F32
+    raise ValueError(f"grad_w must be float32 or bfloat16, is {grad_w.dtype}")
+
+
+def _backward_outputs(G, M, N, K, grad_rows, grad_w, dev_status, workspace, device):
+    """The addresses of grad_rows, grad_w, dev_status and the workspace, and its bytes."""
+    ws, ws_bytes = None, 0
+    if grad_w is not None:
+        needed = ep_expert_backward_workspace_bytes(G, M, N, K)
+        if needed:
+            ws, ws_bytes = _workspace(workspace, device, needed)
+    return (_arg("grad_rows", grad_rows, _BF16, (M, K), device),
+            None if grad_w is None else _arg("grad_w", grad_w, grad_w.dtype, (G, N, K), device),
+            _status(dev_status, device), ws, ws_bytes)
+
+
+def ep_expert_product_bf16_backward(rows, group_offset, w, grad_out, grad_rows, grad_w, dev_status,
+                                    workspace=None, stream=None) -> None:
+    device, st_ = _call_device(stream)
+    if grad_rows is None and grad_w is None:
+        raise ValueError("one of grad_rows and grad_w must be given")
+    if grad_rows is not None:
+        _need("w", w)
+    if grad_w is not None:
+        _need("rows", rows)
+    G, M, N, K, *inputs = _bf16_args(rows, group_offset, w, device, grad_w,
+                                     _need("grad_out", grad_out))
+    st = lib.ep_expert_product_bf16_backward(
+        G, M, N, K, _weights_type(grad_w), *inputs,
+        _arg("grad_out", grad_out, _BF16, (M, N), device),
+        *_backward_outputs(G, M, N, K, grad_rows, grad_w, dev_status, workspace, device), st_)
+    _check(st, "ep_expert_product_bf16_backward")
+
+
+def ep_expert_gate_up_bf16_backward(rows, group_offset, w, pre, grad_out, grad_pre, grad_rows,
+                                    grad_w, dev_status, workspace=None, stream=None) -> None:
+    device, st_ = _call_device(stream)
+    G, M, N, K, *inputs = _bf16_args(_need("rows", rows), group_offset, _need("w", w), device)
+    if N % 16:
+        raise EpError(EP_ERR_INVALID_ARG, "ep_expert_gate_up_bf16_backward")
+    st = lib.ep_expert_gate_up_bf16_backward(
+        G, M, N // 2, K, _weights_type(grad_w), *inputs,
+        _arg("pre", _need("pre", pre), _BF16, (M, N), device),
+        _arg("grad_out", _need("grad_out", grad_out), _BF16, (M, N // 2), device),
+        _arg("grad_pre", _need("grad_pre", grad_pre), _BF16, (M, N), device),
+        *_backward_outputs(G, M, N, K, grad_rows, grad_w, dev_status, workspace, device), st_)
+    _check(st, "ep_expert_gate_up_bf16_backward")
+
+
+class TensorList:
+    """Tensors of float32 and bfloat16 on one device, as ep_grad_norm and ep_grad_clip take
+    them.  Made once for gradients that keep their memory from step to step; it holds that
+    memory, so a tensor that is given other memory (``t.data = ...``) needs a new list.  Tensors
+    that overlap are refused."""
+
+    def __init__(self, tensors):
+        import torch
+        if _U8 is None:
+            _types()
+        keep = [t.detach() for t in tensors]
+        self.device = keep[0].get_device() if keep else None
+        spans = []
+        for i, t in enumerate(keep):
+            if t.dtype is not _F32 and t.dtype is not _BF16:
+                raise ValueError(f"tensor {i} must be float32 or bfloat16, is {t.dtype}")
+            if t.get_device() != self.device or self.device < 0:
+                raise ValueError(f"tensor {i} must be on one GPU with the others, is on {t.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {i} must be contiguous")
+            if t.numel():
+                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i))
+        spans.sort()
+        for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError(f"tensors {i} and {j} overlap")
+        self.tensors = keep
+        self.count = len(keep)
+        self.array = (ep_tensor_t * max(1, self.count))(
+            *[ep_tensor_t(t.data_ptr() if t.numel() else None, t.numel(),
+                          EP_F32 if t.dtype is torch.float32 else EP_BF16, 0) for t in keep])
+
+    def on(self, device, name) -> None:
+        if self.device is not None and self.device != device:
+            raise ValueError(f"{name} must be on the current device ({device}), are on "
+                             f"{self.device}")
+
+
+def _tensor_list(tensors, device, name) -> TensorList:
+    if not isinstance(tensors, TensorList):
+        tensors = TensorList(tensors)
+    tensors.on(device, name)
+    return tensors
+
+
+def ep_grad_norm_workspace_bytes(tensors) -> int:
+    """Of a TensorList, a sequence of tensors or their number."""
+    count = (tensors if isinstance(tensors, int) else
+             tensors.count if isinstance(tensors, TensorList) else len(tensors))
+    return int(lib.ep_grad_norm_workspace_bytes(count))
+
+
+def _sum_squares(t, device):
+    import torch
+    return _arg("sum_squares", _need("sum_squares", t), torch.float64, (1,), device)
+
+
+def ep_grad_norm(tensors, sum_squares, norm, workspace, stream=None) -> None:
+    """tensors: a TensorList, or a sequence of tensors (a list made anew for the call)."""
+    device, st_ = _call_device(stream)
+    tensors = _tensor_list(tensors, device, "tensors")
+    ws, ws_bytes = _workspace(workspace, device, ep_grad_norm_workspace_bytes(tensors))
+    st = lib.ep_grad_norm(tensors.count, tensors.array, _sum_squares(sum_squares, device),
+                          _arg("norm", norm, _F32, (1,), device), ws, ws_bytes, st_)
+    _check(st, "ep_grad_norm")
+
+
+def ep_grad_clip(tensors, sum_squares, max_norm, into=None, stream=None) -> None:
+    device, st_ = _call_device(stream)
+    tensors = _tensor_list(tensors, device, "tensors")
+    into_array = None
+    if into is not None:
+        into = _tensor_list(into, device, "into")
+        if into.count != tensors.count:
+            raise ValueError(f"into must have {tensors.count} tensors, has {into.count}")
+        into_array = into.array
+    st = lib.ep_grad_clip(tensors.count, tensors.array, into_array,
+                          _sum_squares(sum_squares, device), max_norm, st_)
+    _check(st, "ep_grad_clip")
+
+
 class Ring:
     """ep_ring_t: TransferCmd FIFO with `channels` channels of `depth` slots."""
 
@@ -806,3 +1101,106 @@ class BuffersMoE(BuffersLL):
         self.experts(w_gate_up, gate_up_scale, w_down, down_scale)
         self.combine(self.y, self.topk_idx, self.topk_w)
         return self.out
+
+
+class BuffersMoETrain(BuffersLL):
+    """Buffers of a mixture-of-experts block's training pass over per-expert rows in bf16
+    (``s.fmt`` EP_FMT_BF16): norm, router with its balance loss, dispatch, the experts' two
+    products of inner width ``F`` and combine, and their gradients in the opposite order.
+
+    ``forward`` and ``backward`` run on the current stream.  A backward belongs to the forward
+    before it and uses up what that left (self.y and self.pre get their gradients)."""
+
+    def __init__(self, s: ep_shape_t, F: int, capacity_rows: Optional[int] = None,
+                 weights_dtype=None, device="cuda"):
+        import torch
+        if s.fmt != EP_FMT_BF16:
+            raise ValueError("the experts take bf16 rows: fmt must be EP_FMT_BF16")
+        super().__init__(s, capacity_rows, device)
+        T, H, E, k, cap = s.T, s.H, s.E, s.k, self.capacity_rows
+        bf = dict(dtype=torch.bfloat16, device=device)
+        f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
+        wt = dict(dtype=weights_dtype or torch.bfloat16, device=device)
+        self.F = F
+        self.residual = torch.empty((T, H), **bf)
+        self.normed = torch.empty((T, H), **bf)
+        self.rstd = torch.empty(T, **f32)
+        self.topk_idx = torch.empty((T, k), **i32)
+        self.topk_w = torch.empty((T, k), **f32)
+        self.num_choices = torch.empty(E, **i32)
+        self.num_tokens = torch.empty(1, **i32)
+        self.lse = torch.empty(T, **f32)
+        self.balance_loss = torch.empty(1, **f32)
+        self.rows = self.send_buf.view(torch.bfloat16)      # [cap, H]
+        self.pre = torch.empty((cap, 2 * F), **bf)
+        self.inner = torch.empty((cap, F), **bf)
+        self.y = torch.empty((cap, H), **bf)
+        self.grad_topk_w = torch.empty((T, k), **f32)
+        self.grad_inner = torch.empty((cap, F), **bf)
+        self.grad_rows = torch.empty((cap, H), **bf)
+        self.grad_normed = torch.empty((T, H), **bf)
+        self.grad_x = torch.empty((T, H), **bf)
+        self.grad_weight = torch.empty(H, **f32)
+        self.grad_gate_up = torch.empty((E, 2 * F, H), **wt)
+        self.grad_down = torch.empty((E, H, F), **wt)
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.route_workspace = torch.zeros(max(16, ep_route_workspace_bytes(T, E)), **u8)
+        self.back_workspace = torch.empty(
+            max(16, ep_rmsnorm_workspace_bytes(T, H),
+                ep_expert_backward_workspace_bytes(E, cap, 2 * F, H),
+                ep_expert_backward_workspace_bytes(E, cap, H, F)), **u8)
+        self._saved = None
+
+    def forward(self, x, residual, weight, eps, router, w_gate_up, w_down,
+                mode=EP_GATE_SOFTMAX_RENORM, token_mask=None):
+        """router(normed) gives the logits [T, E] (bf16 or float32).  Returns the combined
+        output; self.residual is the residual stream that it belongs to, self.balance_loss the
+        balance loss."""
+        ep_rmsnorm(x, residual, weight, eps, None if residual is None else self.residual,
+                   self.normed, None, self.rstd)
+        if residual is None:
+            self.residual.copy_(x)
+        logits = router(self.normed)
+        ep_route(logits, token_mask, mode, self.topk_idx, self.topk_w, self.num_choices,
+                 self.num_tokens, self.lse, self.balance_loss, self.route_workspace)
+        self.layout(self.topk_idx)
+        self.dispatch(self.normed, self.topk_idx, self.topk_w)
+        ep_expert_gate_up_bf16(self.rows, self.expert_offset, w_gate_up, self.pre, self.inner,
+                               self.dev_status)
+        ep_expert_product_bf16(self.inner, self.expert_offset, w_down, self.y, self.dev_status)
+        self.combine(self.y, self.topk_idx, self.topk_w)
+        self._saved = (weight, w_gate_up, w_down, mode, token_mask, logits)
+        return self.out
+
+    def backward(self, grad_out, grad_residual=None, grad_balance_loss=None, router_backward=None):
+        """grad_out bf16 [T, H]; grad_residual that of self.residual, grad_balance_loss (float32
+        [1], on the device) that of self.balance_loss, or None.  router_backward(grad_logits)
+        gives the gradient of router's input, bf16 [T, H], or None.  Returns the gradient of x (and
+        of residual); the weights' are self.grad_weight, self.grad_gate_up and self.grad_down."""
+        import torch
+        if self._saved is None:
+            raise RuntimeError("backward() needs a forward() before it")
+        weight, w_gate_up, w_down, mode, token_mask, logits = self._saved
+        self._saved = None
+        s, off = self.shape, self.expert_offset
+        ep_combine_ll_backward(s, self.y, self.topk_idx, self.topk_w, self.expert_slot, grad_out,
+                               self.y, self.grad_topk_w, self.dev_status)
+        ep_expert_product_bf16_backward(self.inner, off, w_down, self.y, self.grad_inner,
+                                        self.grad_down, self.dev_status, self.back_workspace)
+        ep_expert_gate_up_bf16_backward(self.rows, off, w_gate_up, self.pre, self.grad_inner,
+                                        self.pre, self.grad_rows, self.grad_gate_up,
+                                        self.dev_status, self.back_workspace)
+        grad_logits = torch.empty_like(logits)
+        ep_route_backward(logits, token_mask, mode, self.topk_idx, self.topk_w, self.num_choices,
+                          self.num_tokens, self.lse, self.grad_topk_w, grad_balance_loss,
+                          grad_logits)
+        other = router_backward(grad_logits) if router_backward is not None else None
+        ep_dispatch_ll_backward(s, self.topk_idx, self.expert_slot, self.grad_rows, None, other,
+                                self.grad_normed, None, self.dev_status)
+        ep_rmsnorm_backward(self.residual, weight, self.rstd, self.grad_normed, grad_residual,
+                            self.grad_x, self.grad_weight, self.back_workspace)
+        return self.grad_x
+
+    def gradients(self):
+        """The weights' gradients, as ep_grad_norm and ep_grad_clip take them."""
+        return TensorList([self.grad_weight, self.grad_gate_up, self.grad_down])

@@ -19,7 +19,7 @@
 
 #include <type_traits>
 
-#include "ep_rows8.h"
+#include "ep_tiles.h"
 
 namespace ep {
 
@@ -36,68 +36,6 @@ struct ExpertArgs {
     int64_t M;                     // rows that `rows` and `out` hold
     int32_t G, N, K, row_bytes, out_bytes, n_tiles;
 };
-
-// Row tiles of bm rows that M rows in G groups can need at most.
-__host__ __device__ inline int64_t max_tiles(int64_t M, int32_t G, int bm) {
-    return M / bm + (G < M ? (int64_t)G : M);
-}
-
-// The rows of a tile of `bm` rows, tiles counted over the groups in order.
-struct RowTile {
-    int32_t g;        // group; -1: no such tile
-    int64_t first;    // first row of the tile
-    int32_t count;    // its rows, 1 .. bm
-};
-
-__device__ inline int64_t clamp_row(int64_t r, int64_t M) { return r < 0 ? 0 : r > M ? M : r; }
-
-// Called by whole wavefronts: lane l looks at group g0 + l, 64 groups a step.
-// Offsets outside [0, M] or decreasing are clamped, so that a tile's rows are
-// always rows of the buffers (check_groups reports them).
-__device__ inline RowTile find_tile(const int32_t* off, int G, int64_t M, int64_t tile, int bm) {
-    RowTile r{-1, 0, 0};
-    const int lane = lane_id();
-    int64_t before = 0;   // tiles of the groups before g0
-    for (int g0 = 0; g0 < G; g0 += kWave) {
-        const int g = g0 + lane;
-        int64_t lo = 0, n = 0;
-        if (g < G) {
-            lo = clamp_row(off[g], M);
-            n = clamp_row(off[g + 1], M) - lo;
-            n = n < 0 ? 0 : n;
-        }
-        const int t = (int)((n + bm - 1) / bm);
-        int sum = t;   // inclusive scan: at most M < 2^31 tiles where the offsets are in order
-#pragma unroll
-        for (int o = 1; o < kWave; o *= 2) {
-            const int up = __shfl_up(sum, o);
-            sum += lane >= o ? up : 0;
-        }
-        const uint64_t here = __ballot(tile < before + sum);
-        if (here) {
-            const int l = __builtin_ctzll(here);
-            const int in = (int)(tile - before) - (bcast(sum, l) - bcast(t, l));
-            // overlapping groups can wrap the sum: such a tile is left out
-            if (in < 0 || in >= bcast(t, l)) return r;
-            r.g = g0 + l;
-            r.first = (int64_t)bcast((int32_t)lo, l) + (int64_t)in * bm;
-            const int64_t left = (int64_t)bcast((int32_t)n, l) - (int64_t)in * bm;
-            r.count = (int)(left < bm ? left : bm);
-            return r;
-        }
-        before += bcast(sum, kWave - 1);
-    }
-    return r;
-}
-
-// Decreasing or negative offsets, and rows beyond M, by the first workgroup.
-__device__ inline void check_groups(const ExpertArgs& a) {
-    for (int g = (int)threadIdx.x; g <= a.G; g += (int)blockDim.x) {
-        const int32_t o = a.group_offset[g];
-        if (o < 0 || (g > 0 && o < a.group_offset[g - 1])) set_error(a.st, EP_ERR_INVALID_ARG);
-        if (o > a.M) set_error(a.st, EP_ERR_CAPACITY);
-    }
-}
 
 __device__ inline i32x8 join(i32x4 lo, i32x4 hi) {
     return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -126,7 +64,7 @@ __device__ inline i32x4 load16(const uint8_t* p) { return *reinterpret_cast<cons
 // resident that loads two or three blocks ahead only cost occupancy (22-25 us).
 __global__ __launch_bounds__(256) void product_small_kernel(ExpertArgs a) {
     __shared__ f32x4 s_acc[4][kWave];
-    if (blockIdx.x == 0) check_groups(a);
+    if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
     const int nt = (int)(blockIdx.x % (unsigned)a.n_tiles);
     const RowTile tile = find_tile(a.group_offset, a.G, a.M, blockIdx.x / (unsigned)a.n_tiles, 16);
     if (tile.g < 0) return;
@@ -193,7 +131,7 @@ __global__ __launch_bounds__(1024) void gate_up_small_kernel(ExpertArgs a) {
     __shared__ float s_sx[2][16][kSlab];
     static_assert(sizeof(float) * 16 * kPitch <= sizeof s_x, "the outputs reuse the rows' LDS");
     float(*const s_y)[kPitch] = reinterpret_cast<float(*)[kPitch]>(s_x);
-    if (blockIdx.x == 0) check_groups(a);
+    if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
     const int fb = (int)(blockIdx.x % (unsigned)a.n_tiles);
     const RowTile tile = find_tile(a.group_offset, a.G, a.M, blockIdx.x / (unsigned)a.n_tiles, 16);
     if (tile.g < 0) return;
@@ -288,45 +226,6 @@ constexpr int kBigGrid = 256;      // CUs of the GPU: one workgroup fills a CU's
 constexpr int kOperandBytes = kBigRows * kScaleBlock;
 constexpr int kRowsAt = 3 * kOperandBytes;      // LDS: three blocks of weights, two of rows
 
-typedef __attribute__((address_space(3))) void* LdsPtr;
-
-// Sixteen bytes a lane from offset `lane_at` + `at` of a buffer to LDS: 64 lanes
-// to 1 KB from `lds` on; `at` and `lds` are the same for the wavefront.
-__device__ inline void to_lds(__amdgpu_buffer_rsrc_t p, uint32_t lane_at, uint32_t at,
-                              uint8_t* lds) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(p, (LdsPtr)lds, 16, (int)lane_at, (int)at, 0, 0);
-}
-
-// Waits until at most VM of the wavefront's memory operations and LDS of its
-// LDS reads are under way (each kind ends in its order), then for the other
-// wavefronts.  (__syncthreads would wait for all the copies.)
-template <int VM, int LDS>
-__device__ inline void meet() {
-    asm volatile("" ::: "memory");
-    // gfx9 encoding: vmcnt in bits 3:0 and 15:14, expcnt 6:4 at its maximum,
-    // lgkmcnt 11:8
-    __builtin_amdgcn_s_waitcnt((VM & 15) | (VM >> 4 << 14) | 0x70 | LDS << 8);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
-// Tiles of all groups.
-__device__ inline int64_t count_tiles(const int32_t* off, int G, int64_t M, int bm) {
-    int64_t all = 0;
-    for (int g0 = 0; g0 < G; g0 += kWave) {
-        const int g = g0 + lane_id();
-        int t = 0;
-        if (g < G) {
-            const int64_t n = clamp_row(off[g + 1], M) - clamp_row(off[g], M);
-            t = n > 0 ? (int)((n + bm - 1) / bm) : 0;
-        }
-#pragma unroll
-        for (int o = 1; o < kWave; o *= 2) t += __shfl_xor(t, o);
-        all += bcast(t, 0);
-    }
-    return all;
-}
-
 // A workgroup's share of the tiles.  Workgroups go to the eight XCDs in turn:
 // each XCD gets one run of the tiles, ordered so that the 32 it has at a time
 // are 5 row tiles x 6 or 7 column tiles, whose operands its L2 shares (8192 x
@@ -378,7 +277,7 @@ __device__ inline void transpose4(uint32_t* c) {
 template <bool GATE>
 __global__ __launch_bounds__(kBigThreads, 2) void product_big_kernel(ExpertArgs a) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[5 * kOperandBytes];
-    if (blockIdx.x == 0) check_groups(a);
+    if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
     // offsets that decrease can count rows many times: no more than M's tiles
     const int64_t counted = count_tiles(a.group_offset, a.G, a.M, kBigRows),
                   most = max_tiles(a.M, a.G, kBigRows);
@@ -684,7 +583,7 @@ constexpr int kMidBytes = kOperandBytes + kMidRows * kScaleBlock;
 template <bool GATE>
 __global__ __launch_bounds__(kBigThreads, 2) void product_mid_kernel(ExpertArgs a) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[kMidStages * kMidBytes];
-    if (blockIdx.x == 0) check_groups(a);
+    if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
     const int nt = (int)(blockIdx.x % (unsigned)a.n_tiles);
     const RowTile tile =
         find_tile(a.group_offset, a.G, a.M, blockIdx.x / (unsigned)a.n_tiles, kMidRows);

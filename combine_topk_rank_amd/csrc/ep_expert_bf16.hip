@@ -1,0 +1,529 @@
+// ep_expert_bf16.hip — the experts' products in bf16, and their gradients: the
+// training form of ep_expert.hip's.
+//
+// Three products over rows grouped by expert, of the same shape: out[q, p] is the
+// sum over c of P and Q.
+//   forward          out[m,n]  = sum_k w[n,k] * rows[m,k]        P = w,    Q = rows
+//   rows' gradient   out[m,k]  = sum_n w[n,k] * grad_out[m,n]    P = w,    Q = grad_out
+//   weights'         out[n,k]  = sum_m rows[m,k] * grad_out[m,n] P = rows, Q = grad_out
+// P is the matrix instruction's first operand and Q its second, so a lane's four
+// results are four neighbouring columns of one row of the output.
+//
+// An operand lies in memory along c (P and Q of the forward, Q of the rows'
+// gradient) or across it (the others).  Either way it is copied as it lies, 16
+// bytes a lane, straight to LDS.  What lies along c is read from LDS 16 bytes a
+// lane; what lies across it is read by the transposing LDS read, which hands each
+// lane four consecutive c of one column.
+//
+// The gate's forward has an output's gate and up in one wavefront and stores
+// silu(gate) * up; its backward makes the gradient of both first, in bf16, and
+// goes on as the plain one.
+
+#include <type_traits>
+
+#include "ep_tiles.h"
+
+namespace ep {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4* LdsS16x4;
+
+enum Product { kForward, kGate, kRowsBack, kWeightBack };
+
+struct Bf16Args {
+    const uint16_t* p;
+    const uint16_t* q;
+    const int32_t* group_offset;   // [G+1]
+    void* out;
+    uint16_t* pre;                 // gate
+    int32_t* st;
+    int64_t M;
+    int64_t tiles;                 // of the launch
+    int32_t G;
+    int32_t W;                     // P's extent outside c (gate: 2F)
+    int32_t V;                     // weights' gradient: Q's extent outside c
+    int32_t C;                     // extent of c (weights' gradient: the group's rows)
+    int32_t pitch_p, pitch_q;      // elements
+    int32_t tiles_w, tiles_v;      // tiles along W, along V
+    int32_t splits;                // weights' gradient: parts of c, each a float output
+    bool wide;                     // weights' gradient: float output
+};
+
+constexpr int kDepth = 64;         // c of a block: 128 bytes of an operand along c
+
+__device__ inline float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+
+__device__ inline f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ inline bf16x8 lds16(const uint8_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// Two transposing reads: lane l of 16 gets column l of the 4 x 16 elements that
+// its 16 lanes point at (8 bytes each), from `p` and from `p` + `next`.
+__device__ inline bf16x8 lds_across(const uint8_t* p, int next) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4)(p + next));
+    return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+}
+
+// ---- Small tiles ------------------------------------------------------------------
+// 64 x 64 outputs a workgroup of four wavefronts, 32 x 32 each; four blocks of c
+// of both operands in LDS, 16 KB each, three under way.
+constexpr int kSmall = 64;
+constexpr int kSmallStages = 4;
+constexpr int kSmallBytes = 2 * kSmall * 128;
+constexpr int kSmallThreads = 256;
+
+template <int MODE>
+__global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a) {
+    constexpr bool kPAcross = MODE == kRowsBack || MODE == kWeightBack;
+    constexpr bool kQAcross = MODE == kWeightBack;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[kSmallStages * kSmallBytes];
+    if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int wp = wave % 2, wq = wave / 2, r = lane % 16, g = lane / 16;
+
+    for (int64_t id = blockIdx.x; id < a.tiles; id += gridDim.x) {
+        // where the tile lies: P from p0 on, Q from q0 on (for the weights'
+        // gradient of expert e, else rows of e), c from block b0 to b1 of the
+        // `depth` values from c0 on
+        const int p0 = (int)(id % a.tiles_w) * (MODE == kGate ? kSmall / 2 : kSmall);
+        int64_t rest = id / a.tiles_w;
+        int e, b0, b1, q_count, part = 0;
+        int64_t q0, c0 = 0, depth = a.C;
+        if constexpr (MODE == kWeightBack) {
+            q0 = (rest % a.tiles_v) * kSmall;
+            rest /= a.tiles_v;
+            part = (int)(rest % a.splits);
+            e = (int)(rest / a.splits);
+            c0 = clamp_row(a.group_offset[e], a.M);
+            depth = clamp_row(a.group_offset[e + 1], a.M) - c0;
+            depth = depth < 0 ? 0 : depth;
+            const int64_t blocks = (depth + kDepth - 1) / kDepth;
+            b0 = (int)(blocks * part / a.splits);
+            b1 = (int)(blocks * (part + 1) / a.splits);
+            q_count = a.V - (int)q0 < kSmall ? a.V - (int)q0 : kSmall;
+        } else {
+            const RowTile tile = find_tile(a.group_offset, a.G, a.M, rest, kSmall);
+            if (tile.g < 0) continue;
+            e = tile.g;
+            q0 = tile.first;
+            q_count = tile.count;
+            b0 = 0;
+            b1 = (a.C + kDepth - 1) / kDepth;
+        }
+
+        // Copies: lane's 16 bytes are chunk `lane % 8` of row 8 (2 wave + i) + lane / 8
+        // of 128 bytes in LDS, i = 0, 1.  Along c: the row is an index of P (Q), and
+        // its chunk c sits at c ^ (row / 2 % 8), so that 16 rows' reads of one chunk
+        // meet all 64 banks once.  Across: the row is a c, and the pairs of chunks that
+        // a 16-column tile takes sit at pair ^ f, f = (c / 2) % 2 + 2 (c / 8 % 2), so
+        // that the 8 rows which half a wavefront reads meet all banks once.
+        // Buffers end behind the last valid row: the rest reads as zero.  Columns
+        // behind a row's last value read the next row's, for outputs that are not
+        // stored; c behind the last is masked.
+        const int row = wave * 16 + lane / 8;
+        const int prow = MODE == kGate ? lane / 8 : row;
+        const int along = (lane % 8) ^ (lane / 16), across = (lane % 8) ^ (lane / 16 % 2 * 2);
+        __amdgpu_buffer_rsrc_t pbuf, qbuf;
+        if constexpr (!kPAcross) {
+            int first = p0, extent = a.W, most = kSmall;
+            if constexpr (MODE == kGate) {    // a wavefront copies 16 gates or 16 ups
+                first = p0 + wave / 2 * 16 + wave % 2 * (a.W / 2);
+                extent = (wave % 2 + 1) * (a.W / 2);
+                most = 16;
+            }
+            first = first < extent ? first : extent - 1;
+            const int rows = extent - first < most ? extent - first : most;
+            pbuf = buffer_rsrc(const_cast<uint16_t*>(a.p) + ((int64_t)e * a.W + first) * a.pitch_p,
+                               rows * a.pitch_p * 2);
+        }
+        if constexpr (!kQAcross)
+            qbuf = buffer_rsrc(const_cast<uint16_t*>(a.q) + q0 * a.pitch_q, q_count * a.pitch_q * 2);
+        const auto fetch = [&](int b, int stage) {
+            b = b < b1 ? b : b1 - 1;          // repeated behind the last block
+            uint8_t* l = s_mem + stage * kSmallBytes + wave * 2048;
+            const int64_t left = depth - (int64_t)b * kDepth;
+            const int rows = left < kDepth ? (int)left : kDepth, chunks = rows / 8;
+            if constexpr (kPAcross) {
+                const int64_t from = MODE == kRowsBack ? (int64_t)e * a.C : c0;
+                pbuf = buffer_rsrc(const_cast<uint16_t*>(a.p) +
+                                       (from + (int64_t)b * kDepth) * a.pitch_p + p0,
+                                   (rows * a.pitch_p - p0) * 2);
+            }
+            if constexpr (kQAcross)
+                qbuf = buffer_rsrc(const_cast<uint16_t*>(a.q) +
+                                       (c0 + (int64_t)b * kDepth) * a.pitch_q + q0,
+                                   (rows * a.pitch_q - (int)q0) * 2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = along ^ (4 * i);
+                uint32_t at = (uint32_t)((prow + 8 * i) * a.pitch_p * 2);
+                if constexpr (kPAcross)
+                    to_lds(pbuf, at + (across ^ (4 * i)) * 16, 0, l + i * 1024);
+                else
+                    to_lds(pbuf, c < chunks ? at + c * 16 : 0x80000000u, b * 128, l + i * 1024);
+                at = (uint32_t)((row + 8 * i) * a.pitch_q * 2);
+                if constexpr (kQAcross)
+                    to_lds(qbuf, at + (across ^ (4 * i)) * 16, 0, l + kSmall * 128 + i * 1024);
+                else
+                    to_lds(qbuf, c < chunks ? at + c * 16 : 0x80000000u, b * 128,
+                           l + kSmall * 128 + i * 1024);
+            }
+        };
+
+        f32x4 acc[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int at0 = r * 128 + (g ^ (r / 2)) * 16;
+        const int f = r / 8 + g % 2 * 2, at_across = (8 * g + r / 4) * 128 + r % 4 * 8;
+        if (b0 < b1) {
+#pragma unroll
+            for (int s = 0; s < kSmallStages - 1; ++s) {
+                fetch(b0 + s, s);
+                __builtin_amdgcn_sched_barrier(0);   // the meetings count on this order
+            }
+            int stage = 0;
+            for (int b = b0; b < b1; ++b) {
+                // block b is here when all but the two behind it are; everyone is then
+                // done with block b - 1, whose place the next copies take
+                meet<4 * (kSmallStages - 2), 0>();
+                fetch(b + kSmallStages - 1, (stage + kSmallStages - 1) % kSmallStages);
+                __builtin_amdgcn_sched_barrier(0);
+                const uint8_t* lp = s_mem + stage * kSmallBytes;
+                const uint8_t* lq = lp + kSmall * 128;
+                bf16x8 p[2][2], q[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int tp = wp * 2 + i, tq = wq * 2 + i;
+                        if constexpr (kPAcross)
+                            p[h][i] = lds_across(lp + h * 4096 + at_across + (tp ^ f) * 32, 512);
+                        else
+                            p[h][i] = lds16(lp + tp * 2048 + (at0 ^ (h * 64)));
+                        if constexpr (kQAcross)
+                            q[h][i] = lds_across(lq + h * 4096 + at_across + (tq ^ f) * 32, 512);
+                        else
+                            q[h][i] = lds16(lq + tq * 2048 + (at0 ^ (h * 64)));
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16(p[h][i], q[h][j], acc[i][j]);
+                stage = (stage + 1) % kSmallStages;
+            }
+            meet<0, 0>();   // the copies behind the last block are in, its reads done
+        }
+
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int qi = wq * 32 + j * 16 + r;
+            if (qi >= q_count) continue;
+            const int64_t qrow = q0 + qi;
+            if constexpr (MODE == kGate) {
+                const int F = a.W / 2, c = p0 + wp * 16 + g * 4;
+                if (c >= F) continue;
+                const f32x4 gate = acc[0][j], up = acc[1][j];
+                float h[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) h[v] = gate[v] * sigmoid(gate[v]) * up[v];
+                *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + qrow * F + c) =
+                    u32x2{bf16_pack(h[0], h[1]), bf16_pack(h[2], h[3])};
+                if (a.pre) {
+                    uint16_t* pre = a.pre + qrow * a.W + c;
+                    *reinterpret_cast<u32x2*>(pre) =
+                        u32x2{bf16_pack(gate[0], gate[1]), bf16_pack(gate[2], gate[3])};
+                    *reinterpret_cast<u32x2*>(pre + F) =
+                        u32x2{bf16_pack(up[0], up[1]), bf16_pack(up[2], up[3])};
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = p0 + wp * 32 + i * 16 + g * 4;
+                    if (c >= a.W) continue;
+                    const f32x4 v = acc[i][j];
+                    if (MODE == kWeightBack && a.wide) {
+                        const int64_t at = (((int64_t)part * a.G + e) * a.V + qrow) * a.W + c;
+                        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at) = v;
+                    } else {
+                        const int64_t at =
+                            (MODE == kWeightBack ? (int64_t)e * a.V + qrow : qrow) * a.W + c;
+                        *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+                            u32x2{bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3])};
+                    }
+                }
+            }
+        }
+    }
+}
+
+// The parts of a weights' gradient, added in their order.
+struct JoinArgs {
+    const f32x4* parts;
+    void* out;
+    int64_t n;        // vectors of 4
+    int32_t splits;
+    bool wide;
+};
+
+__global__ __launch_bounds__(256) void weight_join_kernel(JoinArgs a) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.n; i += (int64_t)gridDim.x * 256) {
+        f32x4 v = a.parts[i];
+        for (int s = 1; s < a.splits; ++s) v += a.parts[s * a.n + i];
+        if (a.wide)
+            reinterpret_cast<f32x4*>(a.out)[i] = v;
+        else
+            reinterpret_cast<u32x2*>(a.out)[i] =
+                u32x2{bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3])};
+    }
+}
+
+// ---- The gate's backward ------------------------------------------------------------
+// grad_gate = d * u * s * (1 + g * (1 - s)), grad_up = d * g * s, s = sigmoid(g).
+// A thread has eight outputs of a row at a time, 2^tpr_log threads a row.
+struct GateBackArgs {
+    const u32x4* pre;        // [M, 2F/8]
+    const u32x4* grad_out;   // [M, F/8]
+    u32x4* grad_pre;
+    const int32_t* group_offset;
+    int32_t* st;
+    int64_t M;
+    int32_t G, nv, tpr_log;
+};
+
+__global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
+    if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
+    const int64_t lo = clamp_row(a.group_offset[0], a.M), end = clamp_row(a.group_offset[a.G], a.M);
+    const int tpr = 1 << a.tpr_log, rpb = 256 >> a.tpr_log;
+    for (int64_t m = lo + (int64_t)blockIdx.x * rpb + ((int)threadIdx.x >> a.tpr_log); m < end;
+         m += (int64_t)gridDim.x * rpb) {
+        for (int c = (int)threadIdx.x & (tpr - 1); c < a.nv; c += tpr) {
+            float gate[8], up[8], d[8];
+            unpack8(a.pre[m * 2 * a.nv + c], gate);
+            unpack8(a.pre[m * 2 * a.nv + a.nv + c], up);
+            unpack8(a.grad_out[m * a.nv + c], d);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float s = sigmoid(gate[q]);
+                const float du = s * fmaf(gate[q], 1.0f - s, 1.0f) * up[q];
+                up[q] = gate[q] * s * d[q];
+                gate[q] = du * d[q];
+            }
+            a.grad_pre[m * 2 * a.nv + c] = pack8(gate);
+            a.grad_pre[m * 2 * a.nv + a.nv + c] = pack8(up);
+        }
+    }
+}
+
+constexpr int kMaxDim = 1 << 20;   // K and N: a tile's rows stay within 32-bit offsets
+
+int check_bf16(int32_t G, int64_t M, int32_t N, int32_t K) {
+    if (G < 1 || G > kMaxE || M < 0 || M >= ((int64_t)1 << 31)) return EP_ERR_INVALID_ARG;
+    if (K < 8 || K % 8 != 0 || K > kMaxDim || N < 8 || N % 8 != 0 || N > kMaxDim)
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+// Parts of c that a weights' gradient is cut into: as many as give two rounds of
+// the CUs, but at least four blocks of the average expert's rows each.
+int32_t weight_splits(int32_t G, int64_t M, int32_t N, int32_t K) {
+    const int64_t tiles = (int64_t)G * ceil_div(N, kSmall) * ceil_div(K, kSmall);
+    const int64_t most = ceil_div(ceil_div(M, G), 4 * kDepth);
+    const int64_t want = ceil_div(1024, tiles);
+    return (int32_t)(want < most ? want : (most < 1 ? 1 : most));
+}
+
+}  // namespace ep
+
+using namespace ep;
+
+namespace {
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+int common_args(Bf16Args& a, int32_t G, int64_t M, const int32_t* group_offset, int32_t* st) {
+    if (!group_offset || !st || (((uintptr_t)group_offset | (uintptr_t)st) & 3))
+        return EP_ERR_INVALID_ARG;
+    a.group_offset = group_offset;
+    a.st = st;
+    a.M = M;
+    a.G = G;
+    a.splits = 1;
+    return EP_OK;
+}
+
+template <int MODE>
+int launch_small(Bf16Args& a, hipStream_t stream) {
+    a.tiles_w = (int32_t)(MODE == kGate ? ceil_div(a.W / 2, kSmall / 2) : ceil_div(a.W, kSmall));
+    if (MODE == kWeightBack) {
+        a.tiles_v = (int32_t)ceil_div(a.V, kSmall);
+        a.tiles = (int64_t)a.G * a.splits * a.tiles_v * a.tiles_w;
+    } else {
+        a.tiles = max_tiles(a.M, a.G, kSmall) * a.tiles_w;
+    }
+    clear_hip_error();
+    hipLaunchKernelGGL(bf16_small_kernel<MODE>, dim3(loop_grid(a.tiles, kSmallThreads)),
+                       dim3(kSmallThreads), 0, stream, a);
+    EP_HIP_CHECK(hipGetLastError());
+    return EP_OK;
+}
+
+int forward(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
+            const int32_t* group_offset, const void* w, void* pre, void* out, int32_t* dev_status,
+            bool gate, hipStream_t stream) {
+    int v = check_bf16(G, M, N, K);
+    if (v != EP_OK) return v;
+    Bf16Args a{};
+    v = common_args(a, G, M, group_offset, dev_status);
+    if (v != EP_OK) return v;
+    if (!w || (M > 0 && (!rows || !out))) return EP_ERR_INVALID_ARG;
+    if (!aligned16(w) || !aligned16(rows) || !aligned16(out) || !aligned16(pre))
+        return EP_ERR_INVALID_ARG;
+    if (M == 0) return EP_OK;
+    a.p = reinterpret_cast<const uint16_t*>(w);
+    a.q = reinterpret_cast<const uint16_t*>(rows);
+    a.out = out;
+    a.pre = reinterpret_cast<uint16_t*>(pre);
+    a.W = N;
+    a.C = a.pitch_p = a.pitch_q = K;
+    return gate ? launch_small<kGate>(a, stream) : launch_small<kForward>(a, stream);
+}
+
+int check_backward(bool any, int32_t dtype, const void* rows, const void* w, const void* grad_rows,
+                   const void* grad_w) {
+    if (dtype != EP_BF16 && dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    if (grad_rows && !w) return EP_ERR_INVALID_ARG;
+    if (grad_w && any && !rows) return EP_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned16(w) || !aligned16(grad_rows) || !aligned16(grad_w))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+// Both gradients, the arguments checked.
+int backward(Bf16Args a, int32_t N, int32_t K, int32_t dtype, const void* rows, const void* w,
+             const void* grad_out, void* grad_rows, void* grad_w, void* workspace,
+             hipStream_t stream) {
+    a.q = reinterpret_cast<const uint16_t*>(grad_out);
+    a.pitch_p = K;
+    a.pitch_q = N;
+    a.W = K;
+    if (grad_rows && a.M > 0) {
+        a.p = reinterpret_cast<const uint16_t*>(w);
+        a.out = grad_rows;
+        a.C = N;
+        const int v = launch_small<kRowsBack>(a, stream);
+        if (v != EP_OK) return v;
+    }
+    if (!grad_w) return EP_OK;
+    a.p = reinterpret_cast<const uint16_t*>(rows);
+    a.V = N;
+    a.splits = weight_splits(a.G, a.M, N, K);
+    a.wide = dtype == EP_F32 || a.splits > 1;
+    a.out = a.splits > 1 ? workspace : grad_w;
+    const int v = launch_small<kWeightBack>(a, stream);
+    if (v != EP_OK || a.splits == 1) return v;
+    JoinArgs j{};
+    j.parts = reinterpret_cast<const f32x4*>(workspace);
+    j.out = grad_w;
+    j.n = (int64_t)a.G * N * K / 4;
+    j.splits = a.splits;
+    j.wide = dtype == EP_F32;
+    const int64_t blocks = ceil_div(j.n, 256);
+    clear_hip_error();
+    hipLaunchKernelGGL(weight_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256),
+                       0, stream, j);
+    EP_HIP_CHECK(hipGetLastError());
+    return EP_OK;
+}
+
+int check_workspace(int32_t G, int64_t M, int32_t N, int32_t K, const void* workspace,
+                    size_t workspace_bytes) {
+    const size_t need = ep_expert_backward_workspace_bytes(G, M, N, K);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+        return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+}  // namespace
+
+extern "C" int ep_expert_product_bf16(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
+                                      const int32_t* group_offset, const void* w, void* out,
+                                      int32_t* dev_status, hipStream_t stream) {
+    return forward(G, M, N, K, rows, group_offset, w, nullptr, out, dev_status, false, stream);
+}
+
+extern "C" int ep_expert_gate_up_bf16(int32_t G, int64_t M, int32_t F, int32_t K, const void* rows,
+                                      const int32_t* group_offset, const void* w, void* pre,
+                                      void* out, int32_t* dev_status, hipStream_t stream) {
+    if (F < 8 || F % 8 != 0 || F > kMaxDim / 2) return EP_ERR_INVALID_ARG;
+    return forward(G, M, 2 * F, K, rows, group_offset, w, pre, out, dev_status, true, stream);
+}
+
+extern "C" size_t ep_expert_backward_workspace_bytes(int32_t G, int64_t M, int32_t N, int32_t K) {
+    if (check_bf16(G, M, N, K) != EP_OK) return 0;
+    const int32_t splits = weight_splits(G, M, N, K);
+    return splits > 1 ? (size_t)splits * G * N * K * 4 : 0;
+}
+
+extern "C" int ep_expert_product_bf16_backward(int32_t G, int64_t M, int32_t N, int32_t K,
+                                               int32_t dtype, const void* rows,
+                                               const int32_t* group_offset, const void* w,
+                                               const void* grad_out, void* grad_rows, void* grad_w,
+                                               int32_t* dev_status, void* workspace,
+                                               size_t workspace_bytes, hipStream_t stream) {
+    int v = check_bf16(G, M, N, K);
+    if (v != EP_OK) return v;
+    Bf16Args a{};
+    v = common_args(a, G, M, group_offset, dev_status);
+    if (v != EP_OK) return v;
+    v = check_backward(M > 0, dtype, rows, w, grad_rows, grad_w);
+    if (v != EP_OK) return v;
+    if (!aligned16(grad_out) || (M > 0 && !grad_out)) return EP_ERR_INVALID_ARG;
+    if (!grad_rows && !grad_w && M > 0) return EP_ERR_INVALID_ARG;
+    if (grad_w && (v = check_workspace(G, M, N, K, workspace, workspace_bytes)) != EP_OK) return v;
+    return backward(a, N, K, dtype, rows, w, grad_out, grad_rows, grad_w, workspace, stream);
+}
+
+extern "C" int ep_expert_gate_up_bf16_backward(int32_t G, int64_t M, int32_t F, int32_t K,
+                                               int32_t dtype, const void* rows,
+                                               const int32_t* group_offset, const void* w,
+                                               const void* pre, const void* grad_out,
+                                               void* grad_pre, void* grad_rows, void* grad_w,
+                                               int32_t* dev_status, void* workspace,
+                                               size_t workspace_bytes, hipStream_t stream) {
+    if (F < 8 || F % 8 != 0 || F > kMaxDim / 2) return EP_ERR_INVALID_ARG;
+    int v = check_bf16(G, M, 2 * F, K);
+    if (v != EP_OK) return v;
+    Bf16Args a{};
+    v = common_args(a, G, M, group_offset, dev_status);
+    if (v != EP_OK) return v;
+    v = check_backward(M > 0, dtype, rows, w, grad_rows, grad_w);
+    if (v != EP_OK) return v;
+    if (!aligned16(pre) || !aligned16(grad_out) || !aligned16(grad_pre)) return EP_ERR_INVALID_ARG;
+    if (M > 0 && (!pre || !grad_out || !grad_pre)) return EP_ERR_INVALID_ARG;
+    if (grad_w && (v = check_workspace(G, M, 2 * F, K, workspace, workspace_bytes)) != EP_OK) return v;
+    if (M > 0) {
+        GateBackArgs b{};
+        b.pre = reinterpret_cast<const u32x4*>(pre);
+        b.grad_out = reinterpret_cast<const u32x4*>(grad_out);
+        b.grad_pre = reinterpret_cast<u32x4*>(grad_pre);
+        b.group_offset = group_offset;
+        b.st = dev_status;
+        b.M = M;
+        b.G = G;
+        b.nv = F / 8;
+        while (b.tpr_log < 8 && (1 << b.tpr_log) < b.nv) ++b.tpr_log;
+        clear_hip_error();
+        hipLaunchKernelGGL(gate_back_kernel, dim3(loop_grid(ceil_div(M, 256 >> b.tpr_log), 256)),
+                           dim3(256), 0, stream, b);
+        EP_HIP_CHECK(hipGetLastError());
+    }
+    return backward(a, 2 * F, K, dtype, rows, w, grad_pre, grad_rows, grad_w, workspace, stream);
+}

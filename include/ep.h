@@ -487,6 +487,143 @@ int ep_expert_gate_up(int32_t G, int64_t M, int32_t F, int32_t K, const void* ro
                       const int32_t* group_offset, const void* w, const float* w_scale,
                       void* out_rows, int32_t* dev_status, hipStream_t stream);
 
+/* ---- The training pass ---------------------------------------------------------
+ * The gradients of combine and dispatch, the experts' products in bf16 with
+ * theirs, and the norm and clipping of all gradients; with ep_route_backward and
+ * ep_rmsnorm_backward they make the backward pass of a mixture-of-experts block.
+ * Tensors are contiguous and, except where a call says so, in- and outputs must
+ * not overlap.  Sums are float (the gradient norm's double), in a fixed order;
+ * each output is rounded once. */
+
+/* Gradient of ep_combine and, per expert, of ep_combine_ll.
+ *   y            bf16 [y_rows,H]: the forward call's, for grad_topk_w
+ *   topk_idx, topk_w, send_slot / expert_slot   the forward call's
+ *   grad_out     bf16 [T,H]
+ *   grad_y       bf16 [y_rows,H], or NULL: row s of token t becomes bf16(W *
+ *                grad_out[t]), W as in the forward call; rows of no token are
+ *                left as they were.  May be y itself.
+ *   grad_topk_w  float [T,k], or NULL (y may be NULL then): the sum of grad_out[t]
+ *                * y[s] over H, s the row of choice j (several choices of one rank
+ *                share a row, and its sum); 0 for a choice without a row
+ * Device error: EP_ERR_CAPACITY if a slot is >= y_rows (that row is skipped). */
+int ep_combine_backward(const ep_shape_t* shape, const void* y, int64_t y_rows,
+                        const int32_t* topk_idx, const float* topk_w, const int32_t* send_slot,
+                        const void* grad_out, void* grad_y, float* grad_topk_w,
+                        int32_t* dev_status, hipStream_t stream);
+int ep_combine_ll_backward(const ep_shape_t* shape, const void* y, int64_t y_rows,
+                           const int32_t* topk_idx, const float* topk_w,
+                           const int32_t* expert_slot, const void* grad_out, void* grad_y,
+                           float* grad_topk_w, int32_t* dev_status, hipStream_t stream);
+
+/* Gradient of a dispatch's rows (ep_dispatch and its fused forms; per expert,
+ * ep_dispatch_ll).
+ *   grad_rows    bf16 [rows,H]: of the rows in send_buf; 8-bit rows' gradient is
+ *                taken as bf16 rows'
+ *   grad_slot_local_w   float [rows,k] (per expert grad_slot_w, float [rows]): of
+ *                the gates that went with the rows, or NULL
+ *   grad_other   bf16 [T,H], or NULL: what reaches x by other ways (a router), added
+ *   grad_x       bf16 [T,H]: grad_other[t] and t's rows, added in the order of
+ *                their ranks (choices).  May be grad_other itself.
+ *   grad_topk_w  float [T,k]: the gate's gradient of the row that serves choice j,
+ *                0 for a choice without one; given if and only if the gates'
+ *                gradient is (NULL where rows = 0)
+ * Device error: EP_ERR_CAPACITY if a slot is >= rows (that row is skipped). */
+int ep_dispatch_backward(const ep_shape_t* shape, const int32_t* topk_idx,
+                         const int32_t* send_slot, const void* grad_rows, int64_t rows,
+                         const float* grad_slot_local_w, const void* grad_other, void* grad_x,
+                         float* grad_topk_w, int32_t* dev_status, hipStream_t stream);
+int ep_dispatch_ll_backward(const ep_shape_t* shape, const int32_t* topk_idx,
+                            const int32_t* expert_slot, const void* grad_rows, int64_t rows,
+                            const float* grad_slot_w, const void* grad_other, void* grad_x,
+                            float* grad_topk_w, int32_t* dev_status, hipStream_t stream);
+
+/* Product of bf16 rows, grouped by expert as in ep_expert_product, with their
+ * experts' bf16 weights.
+ *   rows bf16 [M,K], w bf16 [G,N,K], out bf16 [M,N]: out[m] = rows[m] times w[g]
+ *   transposed; rows of no expert are left as they were
+ * K and N are multiples of 8, 8 to 2^20; G <= 4096, M < 2^31 (M = 0 launches
+ * nothing).  A row's infinities and NaN reach that row alone, an expert's weights'
+ * that expert's rows.  Device errors as at ep_expert_product.  rows, w and out
+ * 16-byte aligned. */
+int ep_expert_product_bf16(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
+                           const int32_t* group_offset, const void* w, void* out,
+                           int32_t* dev_status, hipStream_t stream);
+
+/* Its gradients.
+ *   grad_out   bf16 [M,N]
+ *   grad_rows  bf16 [M,K], or NULL: grad_out[m] times w[g]; rows of no expert are
+ *              left as they were
+ *   grad_w     [G,N,K], dtype EP_BF16 or EP_F32, or NULL: the sum over expert g's
+ *              rows of grad_out[m,n] * rows[m,k]; zero for an expert without rows
+ *   rows is needed for grad_w alone, w for grad_rows alone; NULL otherwise
+ *   workspace  ep_expert_backward_workspace_bytes(G, M, N, K) bytes (0 for most
+ *              shapes), need not be zeroed; for grad_w alone; calls that overlap in
+ *              time need one each
+ * One of grad_rows and grad_w at least. */
+size_t ep_expert_backward_workspace_bytes(int32_t G, int64_t M, int32_t N, int32_t K);
+int ep_expert_product_bf16_backward(int32_t G, int64_t M, int32_t N, int32_t K, int32_t dtype,
+                                    const void* rows, const int32_t* group_offset, const void* w,
+                                    const void* grad_out, void* grad_rows, void* grad_w,
+                                    int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
+/* The first product of a gated expert in bf16: w is [G,2F,K], F gates' rows and
+ * then F ups'; with y = rows times w transposed, in float,
+ *   out[m] = silu(y[m,:F]) * y[m,F:]   bf16 [M,F]
+ *   pre    bf16 [M,2F]: y, for the backward, or NULL
+ * F and K are multiples of 8; F to 2^19, the rest as at ep_expert_product_bf16. */
+int ep_expert_gate_up_bf16(int32_t G, int64_t M, int32_t F, int32_t K, const void* rows,
+                           const int32_t* group_offset, const void* w, void* pre, void* out,
+                           int32_t* dev_status, hipStream_t stream);
+
+/* Its gradients.  With g = pre[m,:F], u = pre[m,F:], s = 1 / (1 + exp(-g)) and
+ * d = grad_out[m] (bf16 [M,F]):
+ *   grad_pre   bf16 [M,2F]: d * u * s * (1 + g * (1 - s)), then d * g * s.  May be
+ *              pre itself.  Rows of no expert are left as they were.
+ *   grad_rows, grad_w   as ep_expert_product_bf16_backward makes them from grad_pre;
+ *              both may be NULL
+ *   workspace  ep_expert_backward_workspace_bytes(G, M, 2F, K) bytes, as there */
+int ep_expert_gate_up_bf16_backward(int32_t G, int64_t M, int32_t F, int32_t K, int32_t dtype,
+                                    const void* rows, const int32_t* group_offset, const void* w,
+                                    const void* pre, const void* grad_out, void* grad_pre,
+                                    void* grad_rows, void* grad_w, int32_t* dev_status,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* A tensor of a list: n elements of dtype EP_BF16 or EP_F32 at data (device
+ * memory, aligned to the element; NULL with n = 0).  n < 2^38. */
+typedef struct ep_tensor {
+    void* data;
+    int64_t n;
+    int32_t dtype;
+    int32_t pad_;
+} ep_tensor_t;
+
+/* The sum of the squares of all elements of `count` tensors (a host array, read
+ * before the call returns), and its root.
+ *   sum_squares double [1], on the device: of a group of GPUs, each its own
+ *               tensors', to be added over them before ep_grad_clip
+ *   norm        float [1], on the device, or NULL: the root
+ *   workspace   ep_grad_norm_workspace_bytes(count) bytes, zero-filled once before
+ *               its first use, left consistent by every call; calls that overlap in
+ *               time need one each
+ * Squares and sums are double: any finite elements have a finite sum (norm is
+ * infinite where the root is beyond float's range).  A tensor may be empty, and
+ * count 0. */
+size_t ep_grad_norm_workspace_bytes(int32_t count);
+int ep_grad_norm(int32_t count, const ep_tensor_t* tensors, double* sum_squares, float* norm,
+                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Every element times max_norm / norm, norm the root of *sum_squares, where norm
+ * is larger than max_norm; as it is otherwise, and where norm is infinite or NaN
+ * (the caller sees that from norm).
+ *   into      NULL: in place.  Otherwise tensors of the same sizes, of either type
+ *             each, that get the values; one may be the tensor itself, but
+ *             otherwise none may overlap another
+ *   max_norm  >= 0
+ * The tensors must not overlap each other. */
+int ep_grad_clip(int32_t count, const ep_tensor_t* tensors, const ep_tensor_t* into,
+                 const double* sum_squares, double max_norm, hipStream_t stream);
+
 /* ---- TransferCmd ring (UCCL-EP s2.2, s2.3, s5.2) ---------------------------
  * `channels` FIFOs of `depth` slots each; a producer blocks while
  * `max_inflight` commands of its channel are published but not yet drained,

@@ -1,0 +1,165 @@
+"""The training pass's calls without a GPU: every refusal is a host-side check
+that launches nothing (the addresses here are not real)."""
+
+import ctypes
+
+import pytest
+
+INVALID = 1
+A = 4096            # an aligned address that is never followed
+
+
+@pytest.fixture(scope="module")
+def ep():
+    import combine_topk_rank_amd as ep
+    return ep
+
+
+def exchange(ep, name, T=4, H=64, E=8, R=4, k=2, fmt=0, **over):
+    s = ep.shape(T, H, E, R, k, fmt)
+    if name.startswith("ep_combine"):
+        a = dict(y=A, rows=9, idx=A, w=A, slot=A, go=A, gy=A, gw=A, st=A)
+    else:
+        a = dict(idx=A, slot=A, gr=A, rows=9, gates=A, other=A, gx=A, gw=A, st=A)
+    a.update(over)
+    return getattr(ep.lib, name)(ctypes.byref(s), *a.values(), None)
+
+
+COMBINE = ["ep_combine_backward", "ep_combine_ll_backward"]
+DISPATCH = ["ep_dispatch_backward", "ep_dispatch_ll_backward"]
+
+
+@pytest.mark.parametrize("name", COMBINE)
+@pytest.mark.parametrize("bad", [
+    dict(T=-1), dict(H=4), dict(H=12), dict(E=9), dict(R=0), dict(R=65, E=65), dict(k=0), dict(k=9), dict(k=33, E=64),
+    dict(fmt=2), dict(fmt=1), dict(y=None), dict(rows=-1), dict(idx=None), dict(w=None), dict(slot=None), dict(go=None),
+    dict(gy=None, gw=None), dict(st=None), dict(y=A + 8), dict(go=A + 4), dict(gy=A + 2), dict(idx=A + 2), dict(w=A + 1),
+    dict(slot=A + 2), dict(gw=A + 2), dict(st=A + 2), dict(T=1 << 30, R=4)])
+def test_combine_refuses(ep, name, bad):
+    assert exchange(ep, name, **bad) == INVALID
+
+
+@pytest.mark.parametrize("name", DISPATCH)
+@pytest.mark.parametrize("bad", [
+    dict(T=-1), dict(H=4), dict(H=12), dict(E=9), dict(R=0), dict(R=65, E=65), dict(k=0), dict(k=9), dict(k=33, E=64),
+    dict(fmt=2), dict(gr=None), dict(rows=-1), dict(idx=None), dict(slot=None), dict(gates=None), dict(gw=None), dict(gx=None),
+    dict(st=None), dict(gr=A + 8), dict(other=A + 4), dict(gx=A + 2), dict(gates=A + 2), dict(gw=A + 1), dict(idx=A + 2),
+    dict(slot=A + 2), dict(st=A + 1)])
+def test_dispatch_refuses(ep, name, bad):
+    assert exchange(ep, name, **bad) == INVALID
+
+
+@pytest.mark.parametrize("name", COMBINE + DISPATCH)
+def test_no_tokens(ep, name):
+    assert exchange(ep, name, T=0) == 0
+    over = dict(y=None, gy=None, gw=None) if name in COMBINE else dict(gr=None, gx=None, gates=None, gw=None, other=None)
+    assert exchange(ep, name, T=0, idx=None, slot=None, **over) == 0
+    assert exchange(ep, name, T=0, st=None) == INVALID
+
+
+def product(L, G=2, M=9, N=64, K=72, rows=A, off=A, w=A, out=A, st=A):
+    return L.ep_expert_product_bf16(G, M, N, K, rows, off, w, out, st, None)
+
+
+def gate(L, G=2, M=9, F=32, K=72, rows=A, off=A, w=A, pre=A, out=A, st=A):
+    return L.ep_expert_gate_up_bf16(G, M, F, K, rows, off, w, pre, out, st, None)
+
+
+SHARED = [dict(G=0), dict(G=4097), dict(M=-1), dict(M=1 << 31), dict(K=0), dict(K=4), dict(K=76), dict(K=(1 << 20) + 8), dict(K=-8),
+          dict(rows=None), dict(off=None), dict(w=None), dict(st=None), dict(rows=A + 8), dict(w=A + 8), dict(off=A + 2),
+          dict(st=A + 2)]
+FORWARD = SHARED + [dict(out=None), dict(out=A + 8)]
+
+
+@pytest.mark.parametrize("bad", FORWARD + [dict(N=0), dict(N=12), dict(N=(1 << 20) + 8)])
+def test_product_refuses(ep, bad):
+    assert product(ep.lib, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", FORWARD + [dict(F=0), dict(F=12), dict(F=(1 << 19) + 8), dict(F=-8), dict(F=1 << 30), dict(pre=A + 8)])
+def test_gate_refuses(ep, bad):
+    assert gate(ep.lib, **bad) == INVALID
+
+
+def test_no_rows_launch_nothing(ep):
+    assert product(ep.lib, M=0) == 0 and product(ep.lib, M=0, rows=None, out=None) == 0
+    assert gate(ep.lib, M=0) == 0 and gate(ep.lib, M=0, rows=None, out=None, pre=None) == 0
+    assert product_back(ep.lib, M=0, gw=None) == 0
+    assert gate_back(ep.lib, M=0, gw=None) == 0
+    assert product(ep.lib, M=0, N=12) == INVALID
+
+
+def product_back(L, G=2, M=9, N=64, K=72, dtype=0, rows=A, off=A, w=A, go=A, gr=A, gw=A, st=A, ws=A, n=1 << 30):
+    return L.ep_expert_product_bf16_backward(G, M, N, K, dtype, rows, off, w, go, gr, gw, st, ws, n, None)
+
+
+def gate_back(L, G=2, M=9, F=32, K=72, dtype=0, rows=A, off=A, w=A, pre=A, go=A, gp=A, gr=A, gw=A, st=A, ws=A, n=1 << 30):
+    return L.ep_expert_gate_up_bf16_backward(G, M, F, K, dtype, rows, off, w, pre, go, gp, gr, gw, st, ws, n, None)
+
+
+BACK = SHARED + [dict(dtype=2), dict(dtype=-1), dict(go=None), dict(go=A + 8), dict(gr=A + 8), dict(gw=A + 4),
+                 dict(G=1, M=100_000, ws=None), dict(G=1, M=100_000, n=64), dict(G=1, M=100_000, ws=A + 8)]
+
+
+@pytest.mark.parametrize("bad", BACK + [dict(N=0), dict(N=12), dict(N=(1 << 20) + 8), dict(gr=None, gw=None)])
+def test_product_backward_refuses(ep, bad):
+    assert product_back(ep.lib, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", BACK + [dict(F=0), dict(F=12), dict(F=(1 << 19) + 8), dict(pre=None), dict(pre=A + 8), dict(gp=None),
+                                        dict(gp=A + 8)])
+def test_gate_backward_refuses(ep, bad):
+    assert gate_back(ep.lib, **bad) == INVALID
+
+
+def test_workspaces(ep):
+    need = ep.ep_expert_backward_workspace_bytes
+    assert need(8, 8192, 7168, 1792) == 0          # tiles enough without parts
+    assert need(1, 100, 64, 64) == 0               # one block of rows
+    assert 0 < need(1, 100_000, 64, 64) < 1 << 26
+    for bad in ((0, 8, 64, 64), (1, -1, 64, 64), (1, 8, 12, 64), (1, 8, 64, 4), (4097, 8, 64, 64), (1, 1 << 31, 64, 64)):
+        assert need(*bad) == 0
+    assert all(need(G, M, N, K) < 1 << 30 for G in (1, 7, 4096) for M in (0, 1, 10 ** 6, 2 ** 31 - 1) for N in (8, 4096) for K in (8, 4096))
+    assert ep.ep_grad_norm_workspace_bytes(0) > 0
+    assert ep.ep_grad_norm_workspace_bytes(1 << 20) < 1 << 26
+    assert ep.ep_grad_norm_workspace_bytes(-1) == 0
+
+
+def tensors(ep, *t):
+    return (ep.ep_tensor_t * max(1, len(t)))(*[ep.ep_tensor_t(*x) for x in t])
+
+
+def norm(ep, t, count=None, s=A, n=A, ws=A, bytes_=1 << 20):
+    return ep.lib.ep_grad_norm(len(t) if count is None else count, t, s, n, ws, bytes_, None)
+
+
+def clip(ep, t, into=None, count=None, s=A, bound=1.0):
+    return ep.lib.ep_grad_clip(len(t) if count is None else count, t, into, s, bound, None)
+
+
+BAD = [(A, -1, 0, 0), (A, 1 << 38, 0, 0), (A, 4, 2, 0), (A, 4, -1, 0), (None, 4, 0, 0), (A + 1, 4, 0, 0), (A + 2, 4, 1, 0)]
+
+
+@pytest.mark.parametrize("bad", BAD)
+def test_a_bad_tensor(ep, bad):
+    good = (A, 8, 1, 0)
+    for t in (tensors(ep, bad), tensors(ep, good, bad)):
+        assert norm(ep, t) == INVALID
+        assert clip(ep, t) == INVALID
+    assert clip(ep, tensors(ep, (A, bad[1] if bad[1] > 0 else 4, 0, 0)), tensors(ep, bad)) == INVALID
+
+
+def test_norm_refuses(ep):
+    t = tensors(ep, (A, 8, 0, 0))
+    for bad in (dict(count=-1), dict(s=None), dict(s=A + 4), dict(n=A + 2), dict(ws=None), dict(ws=A + 8), dict(bytes_=64)):
+        assert norm(ep, t, **bad) == INVALID, bad
+    assert ep.lib.ep_grad_norm(1, None, A, A, A, 1 << 20, None) == INVALID
+
+
+def test_clip_refuses(ep):
+    t = tensors(ep, (A, 8, 0, 0))
+    nan = float("nan")
+    for bad in (dict(count=-1), dict(s=None), dict(s=A + 4), dict(bound=-1.0), dict(bound=nan), dict(into=tensors(ep, (A, 9, 0, 0)))):
+        assert clip(ep, t, **bad) == INVALID, bad
+    assert clip(ep, tensors(ep), count=0) == 0
+    assert clip(ep, tensors(ep, (None, 0, 0, 0), (A, 0, 1, 0))) == 0
