@@ -226,38 +226,6 @@ constexpr int kBigGrid = 256;      // CUs of the GPU: one workgroup fills a CU's
 constexpr int kOperandBytes = kBigRows * kScaleBlock;
 constexpr int kRowsAt = 3 * kOperandBytes;      // LDS: three blocks of weights, two of rows
 
-// A workgroup's share of the tiles.  Workgroups go to the eight XCDs in turn:
-// each XCD gets one run of the tiles, ordered so that the 32 it has at a time
-// are 5 row tiles x 6 or 7 column tiles, whose operands its L2 shares (8192 x
-// 8192 x 7168: 480 us against 486, 496, 486, 500 for 3, 4, 6 and 8).
-constexpr int kBand = 5;
-struct TileShare {
-    int64_t row_tiles, first;   // first: this workgroup's; the next ones follow `step` apart
-    int32_t count, step, n_tiles;
-
-    __device__ TileShare(int64_t row_tiles_, int n_tiles_) {
-        row_tiles = row_tiles_;
-        n_tiles = n_tiles_;
-        const int64_t all = row_tiles * n_tiles, per = all / 8, extra = all % 8;
-        const int xcd = (int)(blockIdx.x % 8u), slot = (int)(blockIdx.x / 8u);
-        step = (int)(gridDim.x / 8u);
-        const int64_t run = per + (xcd < extra);
-        first = xcd * per + (xcd < extra ? xcd : extra) + slot;
-        count = slot < run ? (int)((run - slot + step - 1) / step) : 0;
-    }
-
-    // row tile and column tile of the workgroup's i-th tile
-    __device__ void place(int i, int64_t* m, int* n) const {
-        const int64_t at = first + (int64_t)i * step, wide = kBand * (int64_t)n_tiles;
-        const int64_t band = at / wide;
-        const int in = (int)(at - band * wide);
-        const int64_t left = row_tiles - band * kBand;
-        const int rows = (int)(left < kBand ? left : kBand);
-        *m = band * kBand + in % rows;
-        *n = in / rows;
-    }
-};
-
 // out[k] of lane group g (16 lanes each) = c[g] of lane group k.
 __device__ inline void transpose4(uint32_t* c) {
 #pragma unroll

@@ -62,8 +62,11 @@ __device__ inline f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
 __device__ inline bf16x8 lds16(const uint8_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
 // Two transposing reads: lane l of 16 gets column l of the 4 x 16 elements that
-// its 16 lanes point at (8 bytes each), from `p` and from `p` + `next`.
-__device__ inline bf16x8 lds_across(const uint8_t* p, int next) {
+// its 16 lanes point at (8 bytes each), from `p` and from `p` + `next`.  (`p` is
+// restrict so that the reads carry alias information: without any the compiler
+// waits for all copies to LDS under way before each.)
+__device__ inline __attribute__((always_inline)) bf16x8 lds_across(const uint8_t* __restrict__ p,
+                                                                   int next) {
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4)p);
     const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4)(p + next));
     return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
@@ -265,6 +268,397 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
     }
 }
 
+// ---- Big tiles --------------------------------------------------------------------
+// 256 x 256 outputs a workgroup of eight wavefronts, one workgroup a CU, which
+// works through its share of tiles.  The blocks of c of both operands, 32 KB each,
+// go from memory to LDS ahead of their use, two blocks ahead and on into the next
+// tile: three blocks of P and two of Q fill the 160 KB.  A wavefront has 128 of P
+// x 64 of Q.
+constexpr int kBig = 256;
+constexpr int kBigThreads = 512;
+constexpr int kBigGrid = 256;                   // CUs of the GPU: one workgroup fills a CU's LDS
+constexpr int kOperandBytes = kBig * kDepth * 2;
+constexpr int kQAt = 3 * kOperandBytes;         // LDS: three blocks of P, two of Q
+
+// A workgroup's share of the weights' gradient's tiles, whose depths differ: the
+// experts with most rows first, dealt to the workgroups there and back, so that
+// who had the larger of one round has the smaller of the next.  Neighbours in a
+// round are 32 workgroups of one XCD, bands of 5 tiles along V.  (Up to 64 experts
+// are ordered, a lane each; with more, every workgroup has many.)
+struct WeightShare {
+    int64_t all, per_expert;
+    int32_t count, tiles_w, tiles_v, at;
+    int32_t order;     // lane r: the expert with the r-th most rows
+
+    __device__ WeightShare(const Bf16Args& a) {
+        const int lane = lane_id();
+        order = lane;
+        if (a.G <= kWave) {
+            int n = -1;
+            if (lane < a.G) {
+                const int64_t rows =
+                    clamp_row(a.group_offset[lane + 1], a.M) - clamp_row(a.group_offset[lane], a.M);
+                n = rows < 0 ? 0 : (int)rows;
+            }
+            int rank = 0;
+            for (int g = 0; g < kWave; ++g) {
+                const int m = bcast(n, g);
+                rank += m > n || (m == n && g < lane);
+            }
+            order = __builtin_amdgcn_ds_permute(rank * 4, lane);
+        }
+        tiles_w = a.tiles_w;
+        tiles_v = a.tiles_v;
+        per_expert = (int64_t)tiles_w * tiles_v;
+        all = per_expert * a.G;
+        at = (int)(blockIdx.x % 8u * (gridDim.x / 8u) + blockIdx.x / 8u);
+        const int64_t rounds = all / gridDim.x;
+        count = (int)rounds + (index((int)rounds) < all);
+    }
+    __device__ int64_t index(int i) const {
+        return (int64_t)i * gridDim.x + (i % 2 ? (int)gridDim.x - 1 - at : at);
+    }
+    __device__ void place(const Bf16Args& a, int i, int* e, int* v, int* w) const {
+        const int64_t id = index(i), r = id / per_expert;
+        const int in = (int)(id - r * per_expert), wide = kBand * tiles_w, band = in / wide;
+        const int left = tiles_v - band * kBand, rows = left < kBand ? left : kBand;
+        *e = a.G <= kWave ? bcast(order, (int)r) : (int)r;
+        *v = band * kBand + (in - band * wide) % rows;
+        *w = (in - band * wide) / rows;
+    }
+};
+
+// A tile: P from p0 on, Q from q0 on (q_count of them), `depth` values of c, the
+// first at c0.
+struct BigTile {
+    int64_t q0, c0, depth;
+    int32_t e, p0, q_count, blocks;
+};
+
+template <int MODE>
+__global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
+    constexpr bool kPAcross = MODE == kRowsBack || MODE == kWeightBack;
+    constexpr bool kQAcross = MODE == kWeightBack;
+    constexpr bool kGateUp = MODE == kGate, kWeights = MODE == kWeightBack;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[5 * kOperandBytes];
+    if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int wp = wave % 2, wq = wave / 2;     // neighbours share Q: those without any idle alike
+    const auto share = [&]() {
+        if constexpr (kWeights) {
+            return WeightShare(a);
+        } else {
+            // offsets that decrease can count rows many times: no more than M's tiles
+            const int64_t counted = count_tiles(a.group_offset, a.G, a.M, kBig),
+                          most = max_tiles(a.M, a.G, kBig);
+            return TileShare(counted < most ? counted : most, a.tiles_w);
+        }
+    }();
+    const auto tile_at = [&](int i) {
+        BigTile t;
+        if constexpr (kWeights) {
+            int v, w;
+            share.place(a, i, &t.e, &v, &w);
+            t.p0 = w * kBig;
+            t.q0 = (int64_t)v * kBig;
+            t.q_count = a.V - v * kBig < kBig ? a.V - v * kBig : kBig;
+            t.c0 = clamp_row(a.group_offset[t.e], a.M);
+            t.depth = clamp_row(a.group_offset[t.e + 1], a.M) - t.c0;
+            if (t.depth < 0) t.depth = 0;
+        } else {
+            int64_t m;
+            int n;
+            share.place(i, &m, &n);
+            const RowTile r = find_tile(a.group_offset, a.G, a.M, m, kBig);
+            t.e = r.g < 0 ? 0 : r.g;
+            t.p0 = n * (kGateUp ? kBig / 2 : kBig);
+            t.q0 = r.g < 0 ? 0 : r.first;
+            t.q_count = r.g < 0 ? 0 : r.count;
+            t.c0 = 0;
+            t.depth = a.C;
+        }
+        t.blocks = (int)((t.depth + kDepth - 1) / kDepth);
+        return t;
+    };
+
+    // Where the copies stand: block `fb` of tile `ft`.  Along c a wavefront copies
+    // rows wave * 32 + 8 i + lane / 8 of an operand, chunk c of row q to chunk
+    // c ^ (q / 2 % 8) of its 128 bytes.  Across, c's of a block are rows of 512 bytes,
+    // two an instruction, wave * 8 + 2 i + lane / 32; the 32 bytes of row c which a
+    // tile of 16 columns takes sit at ^ f, f = c % 4 + 4 (c / 8 % 2), so that the
+    // eight rows which half a wavefront reads meet all banks once.  The buffers' ends
+    // and what lies behind them are as in the small tiles.
+    int ft = 0, fb = 0;
+    BigTile to{};
+    __amdgpu_buffer_rsrc_t pbuf, qbuf;
+    uint32_t op[2], oq[2];         // this lane's offsets for even and odd i
+    const uint32_t pitch_p = (uint32_t)a.pitch_p * 2, pitch_q = (uint32_t)a.pitch_q * 2;
+    const auto aim_block = [&]() {
+        const int64_t left = to.depth - (int64_t)fb * kDepth;
+        const int rows = left < kDepth ? (int)left : kDepth, chunks = rows / 8;
+        if constexpr (kPAcross) {
+            const int64_t from = kWeights ? to.c0 : (int64_t)to.e * a.C;
+            pbuf = buffer_rsrc(const_cast<uint16_t*>(a.p) +
+                                   (from + (int64_t)fb * kDepth) * a.pitch_p + to.p0,
+                               (rows * a.pitch_p - to.p0) * 2);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = (lane % 8) ^ (lane / 16) ^ (4 * i);
+                op[i] = c < chunks ? (uint32_t)(lane / 8) * pitch_p + c * 16 : 0x80000000u;
+            }
+        }
+        if constexpr (kQAcross) {
+            qbuf = buffer_rsrc(const_cast<uint16_t*>(a.q) +
+                                   (to.c0 + (int64_t)fb * kDepth) * a.pitch_q + to.q0,
+                               (rows * a.pitch_q - (int)to.q0) * 2);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = (lane % 8) ^ (lane / 16) ^ (4 * i);
+                oq[i] = c < chunks ? (uint32_t)(wave * 32 + lane / 8) * pitch_q + c * 16 : 0x80000000u;
+            }
+        }
+    };
+    const auto aim = [&]() {
+        if constexpr (!kPAcross) {
+            // this wavefront's 32 rows of P: for the gate 32 of the 64 gates or ups that a
+            // wavefront's 128 rows have
+            const int half = kGateUp ? wave % 4 / 2 : 0, F = a.W / 2;
+            const int first = kGateUp ? half * F + to.p0 + wave / 4 * 64 + wave % 2 * 32
+                                      : to.p0 + wave * 32;
+            const int extent = kGateUp ? (half + 1) * F : a.W;
+            const int base = first < extent ? first : extent - 1;
+            const int rows = extent - base < 32 ? extent - base : 32;
+            pbuf = buffer_rsrc(const_cast<uint16_t*>(a.p) + ((int64_t)to.e * a.W + base) * a.pitch_p,
+                               rows * a.pitch_p * 2);
+        }
+        if constexpr (!kQAcross)
+            qbuf = buffer_rsrc(const_cast<uint16_t*>(a.q) + to.q0 * a.pitch_q,
+                               (to.q_count < 1 ? 1 : to.q_count) * a.pitch_q * 2);
+        aim_block();
+    };
+    if constexpr (kPAcross) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            op[i] = (uint32_t)(wave * 8 + lane / 32) * pitch_p +
+                    ((lane % 32) ^ (lane / 32 * 2) ^ (i * 4) ^ (wave % 2 * 8)) * 16;
+    }
+    if constexpr (kQAcross) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            oq[i] = (uint32_t)(wave * 8 + lane / 32) * pitch_q +
+                    ((lane % 32) ^ (lane / 32 * 2) ^ (i * 4) ^ (wave % 2 * 8)) * 16;
+    }
+    // behind the last tile the copies repeat its last block
+    const auto advance = [&]() {
+        if (++fb < to.blocks) {
+            aim_block();
+            return;
+        }
+        int next = ft + 1;
+        BigTile t{};
+        for (; next < share.count; ++next) {
+            t = tile_at(next);
+            if (!kWeights || t.blocks > 0) break;
+        }
+        if (next < share.count) {
+            ft = next;
+            to = t;
+            fb = 0;
+            aim();
+        } else {
+            fb = to.blocks - 1;
+        }
+    };
+    const auto fetch_p = [&](uint32_t at, int i) {
+        to_lds(pbuf, op[i % 2] + (uint32_t)i * (kPAcross ? 2 : 8) * pitch_p,
+               kPAcross ? 0 : fb * 128, s_mem + at + wave * 4096 + i * 1024);
+    };
+    const auto fetch_q = [&](uint32_t at, int i) {
+        to_lds(qbuf, oq[i % 2] + (uint32_t)i * (kQAcross ? 2 : 8) * pitch_q,
+               kQAcross ? 0 : fb * 128, s_mem + at + wave * 4096 + i * 1024);
+    };
+
+    // Reads: lane's column of P (Q) is r = lane % 16 of a tile of 16, its c's are 8 g on,
+    // g = lane / 16, in each half of a block.
+    const int r = lane % 16, g = lane / 16;
+    const int along = r * 128 + (g ^ (r / 2)) * 16;
+    const int fold = r / 4 + g % 2 * 4, across = (8 * g + r / 4) * 512 + r % 4 * 8;
+    const int across_p = across + ((wp * 8) ^ fold) * 32, across_q = across + ((wq * 4) ^ fold) * 32;
+    const auto ptile = [&](uint32_t at, int i, int h) {
+        if constexpr (kPAcross)
+            return lds_across(s_mem + at + (across_p ^ (i * 32)) + h * 16384, 2048);
+        else
+            return lds16(s_mem + at + wp * 16384 + i * 2048 + (along ^ (h * 64)));
+    };
+    const auto qtile = [&](uint32_t at, int j, int h) {
+        if constexpr (kQAcross)
+            return lds_across(s_mem + at + (across_q ^ (j * 32)) + h * 16384, 2048);
+        else
+            return lds16(s_mem + at + wq * 8192 + j * 2048 + (along ^ (h * 64)));
+    };
+
+    // the first tile with a block
+    bool any = false;
+    for (; ft < share.count && !any; ft += !any) {
+        to = tile_at(ft);
+        any = to.blocks > 0;
+    }
+
+    // places of this, the next and the over-next block
+    uint32_t p_at[3] = {0, kOperandBytes, 2 * kOperandBytes};
+    uint32_t q_at[2] = {kQAt, kQAt + kOperandBytes};
+    f32x4 acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    bf16x8 p[3][2], q[2][4];
+    if (any) {
+        aim();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            fetch_p(p_at[0], i);
+            fetch_q(q_at[0], i);
+        }
+        meet<0, 0>();
+        advance();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            fetch_p(p_at[1], i);
+            fetch_q(q_at[1], i);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[h][j] = qtile(q_at[0], j, h);
+            p[0][h] = ptile(p_at[0], 0, h);
+        }
+    }
+
+    // One block: eight P tiles, eight MFMAs each.  P is read two tiles ahead.  Two
+    // meetings: at i = 1 every wavefront has its Q in registers, and their place takes
+    // Q of the block two ahead; at i = 6 every wavefront has read its P and the next
+    // block has arrived (all but the eight copies of the one after it), whose first
+    // reads follow under the MFMAs left.  A wavefront without any Q copies and meets
+    // only.
+    const auto block = [&](auto busy) {
+        constexpr int kReads = kPAcross ? 4 : 2;    // LDS reads of a tile of P
+        const auto read_p = [&](uint32_t at, int i, int to_reg) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) p[to_reg][h] = ptile(at, i, h);
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (busy.value) {
+                if (i == 0) read_p(p_at[0], 1, 1);
+                // the reads of P tile 2 may be under way, not Q's
+                if (i == 1) meet<63, kReads>();
+                if (i < 6) read_p(p_at[0], i + 2, (i + 2) % 3);
+            } else {
+                if (i == 1) meet<63, 0>();
+            }
+            if (i < 4) fetch_p(p_at[2], i);
+            if (i >= 2 && i < 6) fetch_q(q_at[0], i - 2);
+            if (i == 6) meet<8, 0>();
+            if (i == 7) read_p(p_at[1], 0, 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (busy.value) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        acc[i][j] = mfma_bf16(p[i % 3][h], q[h][j], acc[i][j]);
+                    }
+                    if (i == 7) q[h][j] = qtile(q_at[1], j, h);
+                }
+        }
+        if constexpr (busy.value) __builtin_amdgcn_sched_barrier(0);
+        const uint32_t p0 = p_at[0], q0 = q_at[0];
+        p_at[0] = p_at[1];
+        p_at[1] = p_at[2];
+        p_at[2] = p0;
+        q_at[0] = q_at[1];
+        q_at[1] = q0;
+    };
+
+    for (int ti = 0; ti < share.count; ++ti) {
+        const BigTile t = tile_at(ti);
+        const bool busy = wq * 64 < t.q_count;
+        for (int b = 0; b < t.blocks; ++b) {
+            advance();
+            if (busy)
+                block(std::true_type{});
+            else
+                block(std::false_type{});
+        }
+        if (busy) {
+            // (opaque: addresses made from them are not worth registers in the loop)
+            int row = lane % 16, group = lane / 16;
+            asm volatile("" : "+v"(row), "+v"(group));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int qi = wq * 64 + j * 16 + row;
+                const int64_t qrow = t.q0 + qi;
+                const bool in = qi < t.q_count;
+                // A lane has columns 4 group .. 4 group + 3 of each 16: two neighbouring
+                // tiles' halves change hands, so that it has 8 of one of them.
+                const auto store8 = [&](const f32x4& v, const f32x4& w, uint16_t* out, int first,
+                                        int end) {
+                    const u32x2 lo = __builtin_amdgcn_permlane16_swap(
+                        bf16_pack(v[0], v[1]), bf16_pack(w[0], w[1]), false, false);
+                    const u32x2 hi = __builtin_amdgcn_permlane16_swap(
+                        bf16_pack(v[2], v[3]), bf16_pack(w[2], w[3]), false, false);
+                    const int c = first + group % 2 * 16 + group / 2 * 8;
+                    if (in && c < end)
+                        *reinterpret_cast<u32x4*>(out + c) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                };
+                if constexpr (kGateUp) {
+                    const int F = a.W / 2;
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        const int first = t.p0 + wp * 64 + i * 16;
+                        if (a.pre) {
+                            uint16_t* pre = a.pre + qrow * a.W;
+                            store8(acc[i][j], acc[i + 1][j], pre, first, F);
+                            store8(acc[i + 4][j], acc[i + 5][j], pre + F, first, F);
+                        }
+#pragma unroll
+                        for (int k = i; k < i + 2; ++k)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                acc[k][j][v] *= sigmoid(acc[k][j][v]) * acc[k + 4][j][v];
+                        store8(acc[i][j], acc[i + 1][j],
+                               reinterpret_cast<uint16_t*>(a.out) + qrow * F, first, F);
+                    }
+                } else {
+                    const int64_t at = (kWeights ? (int64_t)t.e * a.V + qrow : qrow) * a.W;
+                    const int first = t.p0 + wp * 128;
+                    if (kWeights && a.wide) {
+                        float* out = reinterpret_cast<float*>(a.out) + at;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int c = first + i * 16 + group * 4;
+                            if (in && c < a.W) *reinterpret_cast<f32x4*>(out + c) = acc[i][j];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2)
+                            store8(acc[i][j], acc[i + 1][j], reinterpret_cast<uint16_t*>(a.out) + at,
+                                   first + i * 16, a.W);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    wait_vm();   // no copy may reach the LDS after the workgroup's end
+}
+
 // The parts of a weights' gradient, added in their order.
 struct JoinArgs {
     const f32x4* parts;
@@ -289,6 +683,16 @@ __global__ __launch_bounds__(256) void weight_join_kernel(JoinArgs a) {
 // ---- The gate's backward ------------------------------------------------------------
 // grad_gate = d * u * s * (1 + g * (1 - s)), grad_up = d * g * s, s = sigmoid(g).
 // A thread has eight outputs of a row at a time, 2^tpr_log threads a row.
+// d's products come first: of two bf16 values they are exact in float.  Each
+// operation is rounded by itself (no fused multiply-add), as elementary float
+// operations are.
+__device__ inline void gate_back(float& gate, float& up, float d) {
+#pragma clang fp contract(off)
+    const float s = sigmoid(gate), g = gate;
+    gate = d * up * s * (1.0f + g * (1.0f - s));
+    up = d * g * s;
+}
+
 struct GateBackArgs {
     const u32x4* pre;        // [M, 2F/8]
     const u32x4* grad_out;   // [M, F/8]
@@ -311,12 +715,7 @@ __global__ __launch_bounds__(256) void gate_back_kernel(GateBackArgs a) {
             unpack8(a.pre[m * 2 * a.nv + a.nv + c], up);
             unpack8(a.grad_out[m * a.nv + c], d);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float s = sigmoid(gate[q]);
-                const float du = s * fmaf(gate[q], 1.0f - s, 1.0f) * up[q];
-                up[q] = gate[q] * s * d[q];
-                gate[q] = du * d[q];
-            }
+            for (int q = 0; q < 8; ++q) gate_back(gate[q], up[q], d[q]);
             a.grad_pre[m * 2 * a.nv + c] = pack8(gate);
             a.grad_pre[m * 2 * a.nv + a.nv + c] = pack8(up);
         }
@@ -376,6 +775,35 @@ int launch_small(Bf16Args& a, hipStream_t stream) {
     return EP_OK;
 }
 
+// A workgroup a CU, or, for fewer tiles, one each, in whole eights for the XCDs
+// that share them out.
+template <int MODE>
+int launch_big(Bf16Args& a, hipStream_t stream) {
+    a.tiles_w = (int32_t)(MODE == kGate ? ceil_div(a.W / 2, kBig / 2) : ceil_div(a.W, kBig));
+    if (MODE == kWeightBack) {
+        a.tiles_v = (int32_t)ceil_div(a.V, kBig);
+        a.tiles = (int64_t)a.G * a.tiles_v * a.tiles_w;
+    } else {
+        a.tiles = max_tiles(a.M, a.G, kBig) * a.tiles_w;
+    }
+    if (a.tiles >= ((int64_t)1 << 31)) {
+        record_error("expert product: more than 2^31 tiles");
+        return EP_ERR_INVALID_ARG;
+    }
+    clear_hip_error();
+    hipLaunchKernelGGL(bf16_big_kernel<MODE>,
+                       dim3((unsigned)(a.tiles < kBigGrid ? ceil_div(a.tiles, 8) * 8 : kBigGrid)),
+                       dim3(kBigThreads), 0, stream, a);
+    EP_HIP_CHECK(hipGetLastError());
+    return EP_OK;
+}
+
+template <int MODE>
+int launch(Bf16Args& a, hipStream_t stream) {
+    if (a.M >= (int64_t)a.G * 128 && a.splits == 1) return launch_big<MODE>(a, stream);
+    return launch_small<MODE>(a, stream);
+}
+
 int forward(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
             const int32_t* group_offset, const void* w, void* pre, void* out, int32_t* dev_status,
             bool gate, hipStream_t stream) {
@@ -394,7 +822,7 @@ int forward(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
     a.pre = reinterpret_cast<uint16_t*>(pre);
     a.W = N;
     a.C = a.pitch_p = a.pitch_q = K;
-    return gate ? launch_small<kGate>(a, stream) : launch_small<kForward>(a, stream);
+    return gate ? launch<kGate>(a, stream) : launch<kForward>(a, stream);
 }
 
 int check_backward(bool any, int32_t dtype, const void* rows, const void* w, const void* grad_rows,
@@ -419,7 +847,7 @@ int backward(Bf16Args a, int32_t N, int32_t K, int32_t dtype, const void* rows, 
         a.p = reinterpret_cast<const uint16_t*>(w);
         a.out = grad_rows;
         a.C = N;
-        const int v = launch_small<kRowsBack>(a, stream);
+        const int v = launch<kRowsBack>(a, stream);
         if (v != EP_OK) return v;
     }
     if (!grad_w) return EP_OK;
@@ -428,7 +856,7 @@ int backward(Bf16Args a, int32_t N, int32_t K, int32_t dtype, const void* rows, 
     a.splits = weight_splits(a.G, a.M, N, K);
     a.wide = dtype == EP_F32 || a.splits > 1;
     a.out = a.splits > 1 ? workspace : grad_w;
-    const int v = launch_small<kWeightBack>(a, stream);
+    const int v = launch<kWeightBack>(a, stream);
     if (v != EP_OK || a.splits == 1) return v;
     JoinArgs j{};
     j.parts = reinterpret_cast<const f32x4*>(workspace);
