@@ -53,7 +53,13 @@ struct Bf16Args {
 
 constexpr int kDepth = 64;         // c of a block: 128 bytes of an operand along c
 
-__device__ inline float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// 1 / (1 + exp(-g)); far below zero exp(g), which is the same there: exp(-g) leaves
+// float's range at -88.7, where times a large up the product is still a number.
+__device__ inline float sigmoid(float g) {
+    const bool far = g < -80.0f;
+    const float e = expf(far ? g : -g);
+    return far ? e : 1.0f / (1.0f + e);
+}
 
 __device__ inline f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -275,10 +281,22 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
 // tile: three blocks of P and two of Q fill the 160 KB.  A wavefront has 128 of P
 // x 64 of Q.
 constexpr int kBig = 256;
-constexpr int kBigThreads = 512;
+constexpr int kBigWaves = 4;
+constexpr int kBigThreads = kBigWaves * kWave;
+constexpr int kBigCopies = 32 / kBigWaves;      // a wavefront's copies of a block of an operand
+constexpr int kBigQTiles = 32 / kBigWaves;      // its tiles of 16 along Q
 constexpr int kBigGrid = 256;                   // CUs of the GPU: one workgroup fills a CU's LDS
 constexpr int kOperandBytes = kBig * kDepth * 2;
 constexpr int kQAt = 3 * kOperandBytes;         // LDS: three blocks of P, two of Q
+
+// A value that all lanes have, in scalar registers whatever it was made from: what
+// a buffer is made of has to be.
+__device__ inline int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline bool uniform(bool v) { return __builtin_amdgcn_readfirstlane((int)v); }
+__device__ inline int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int32_t)(v >> 32)) << 32 |
+                     (uint32_t)uniform((int32_t)v));
+}
 
 // A workgroup's share of the weights' gradient's tiles, whose depths differ: the
 // experts with most rows first, dealt to the workgroups there and back, so that
@@ -335,8 +353,8 @@ struct BigTile {
     int32_t e, p0, q_count, blocks;
 };
 
-template <int MODE>
-__global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
+template <int MODE, bool WIDE>
+__global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void bf16_big_kernel(Bf16Args a) {
     constexpr bool kPAcross = MODE == kRowsBack || MODE == kWeightBack;
     constexpr bool kQAcross = MODE == kWeightBack;
     constexpr bool kGateUp = MODE == kGate, kWeights = MODE == kWeightBack;
@@ -351,9 +369,17 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
             // offsets that decrease can count rows many times: no more than M's tiles
             const int64_t counted = count_tiles(a.group_offset, a.G, a.M, kBig),
                           most = max_tiles(a.M, a.G, kBig);
-            return TileShare(counted < most ? counted : most, a.tiles_w);
+            return TileShare(uniform(counted < most ? counted : most), a.tiles_w);
         }
     }();
+    // the first 64 groups' offsets, a lane each: a tile's start costs no load then (its
+    // wait would be a wait for the copies)
+    int64_t lo = 0, rows_here = 0;
+    if (lane < a.G) {
+        lo = clamp_row(a.group_offset[lane], a.M);
+        rows_here = clamp_row(a.group_offset[lane + 1], a.M) - lo;
+        rows_here = rows_here < 0 ? 0 : rows_here;
+    }
     const auto tile_at = [&](int i) {
         BigTile t;
         if constexpr (kWeights) {
@@ -362,14 +388,22 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
             t.p0 = w * kBig;
             t.q0 = (int64_t)v * kBig;
             t.q_count = a.V - v * kBig < kBig ? a.V - v * kBig : kBig;
-            t.c0 = clamp_row(a.group_offset[t.e], a.M);
-            t.depth = clamp_row(a.group_offset[t.e + 1], a.M) - t.c0;
-            if (t.depth < 0) t.depth = 0;
+            if (t.e < kWave) {
+                t.c0 = bcast((int32_t)lo, t.e);
+                t.depth = bcast((int32_t)rows_here, t.e);
+            } else {
+                t.c0 = clamp_row(a.group_offset[t.e], a.M);
+                t.depth = clamp_row(a.group_offset[t.e + 1], a.M) - t.c0;
+                if (t.depth < 0) t.depth = 0;
+            }
         } else {
             int64_t m;
             int n;
             share.place(i, &m, &n);
-            const RowTile r = find_tile(a.group_offset, a.G, a.M, m, kBig);
+            RowTile r{-1, 0, 0};
+            int64_t before = 0;
+            if (!find_in(lo, rows_here, 0, &before, m, kBig, &r) && a.G > kWave)
+                r = find_tile(a.group_offset, a.G, a.M, m, kBig);
             t.e = r.g < 0 ? 0 : r.g;
             t.p0 = n * (kGateUp ? kBig / 2 : kBig);
             t.q0 = r.g < 0 ? 0 : r.first;
@@ -377,6 +411,12 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
             t.c0 = 0;
             t.depth = a.C;
         }
+        t.q0 = uniform(t.q0);
+        t.c0 = uniform(t.c0);
+        t.depth = uniform(t.depth);
+        t.e = uniform(t.e);
+        t.p0 = uniform(t.p0);
+        t.q_count = uniform(t.q_count);
         t.blocks = (int)((t.depth + kDepth - 1) / kDepth);
         return t;
     };
@@ -391,45 +431,43 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
     int ft = 0, fb = 0;
     BigTile to{};
     __amdgpu_buffer_rsrc_t pbuf, qbuf;
-    uint32_t op[2], oq[2];         // this lane's offsets for even and odd i
+    uint32_t op[4], oq[4];         // this lane's offsets, by i % 2 and, across, also i / 4 % 2
     const uint32_t pitch_p = (uint32_t)a.pitch_p * 2, pitch_q = (uint32_t)a.pitch_q * 2;
+    const uint16_t *pb = nullptr, *qb = nullptr;    // across: where block fb begins
     const auto aim_block = [&]() {
         const int64_t left = to.depth - (int64_t)fb * kDepth;
-        const int rows = left < kDepth ? (int)left : kDepth, chunks = rows / 8;
+        const int rows = left < kDepth ? (int)left : kDepth;
         if constexpr (kPAcross) {
             const int64_t from = kWeights ? to.c0 : (int64_t)to.e * a.C;
-            pbuf = buffer_rsrc(const_cast<uint16_t*>(a.p) +
-                                   (from + (int64_t)fb * kDepth) * a.pitch_p + to.p0,
-                               (rows * a.pitch_p - to.p0) * 2);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = (lane % 8) ^ (lane / 16) ^ (4 * i);
-                op[i] = c < chunks ? (uint32_t)(lane / 8) * pitch_p + c * 16 : 0x80000000u;
-            }
+            pb = a.p + (from + (int64_t)fb * kDepth) * a.pitch_p + to.p0;
+            pbuf = buffer_rsrc(const_cast<uint16_t*>(pb), (rows * a.pitch_p - to.p0) * 2);
         }
         if constexpr (kQAcross) {
-            qbuf = buffer_rsrc(const_cast<uint16_t*>(a.q) +
-                                   (to.c0 + (int64_t)fb * kDepth) * a.pitch_q + to.q0,
-                               (rows * a.pitch_q - (int)to.q0) * 2);
-        } else {
+            qb = a.q + (to.c0 + (int64_t)fb * kDepth) * a.pitch_q + to.q0;
+            qbuf = buffer_rsrc(const_cast<uint16_t*>(qb), (rows * a.pitch_q - (int)to.q0) * 2);
+        }
+        if (!kQAcross && a.C % kDepth != 0 && (fb == 0 || fb == to.blocks - 1)) {
+            // c behind the last is masked: only in a last block, undone in a first
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = (lane % 8) ^ (lane / 16) ^ (4 * i);
-                oq[i] = c < chunks ? (uint32_t)(wave * 32 + lane / 8) * pitch_q + c * 16 : 0x80000000u;
+                // (the sign, not a choice: that becomes a branch, and what follows divergent)
+                const uint32_t past = (uint32_t)(rows / 8 - 1 - c) & 0x80000000u;
+                if constexpr (!kPAcross) op[i] = ((uint32_t)(lane / 8) * pitch_p + c * 16) | past;
+                oq[i] = ((uint32_t)(wave * 8 * kBigCopies + lane / 8) * pitch_q + c * 16) | past;
             }
         }
     };
     const auto aim = [&]() {
         if constexpr (!kPAcross) {
-            // this wavefront's 32 rows of P: for the gate 32 of the 64 gates or ups that a
-            // wavefront's 128 rows have
-            const int half = kGateUp ? wave % 4 / 2 : 0, F = a.W / 2;
-            const int first = kGateUp ? half * F + to.p0 + wave / 4 * 64 + wave % 2 * 32
-                                      : to.p0 + wave * 32;
+            // this wavefront's rows of P: for the gate some of the 64 gates or 64 ups that 128
+            // rows have
+            constexpr int kRows = 8 * kBigCopies;
+            const int at = wave * kRows, half = kGateUp ? at % 128 / 64 : 0, F = a.W / 2;
+            const int first = kGateUp ? half * F + to.p0 + at / 128 * 64 + at % 64 : to.p0 + at;
             const int extent = kGateUp ? (half + 1) * F : a.W;
             const int base = first < extent ? first : extent - 1;
-            const int rows = extent - base < 32 ? extent - base : 32;
+            const int rows = extent - base < kRows ? extent - base : kRows;
             pbuf = buffer_rsrc(const_cast<uint16_t*>(a.p) + ((int64_t)to.e * a.W + base) * a.pitch_p,
                                rows * a.pitch_p * 2);
         }
@@ -438,46 +476,59 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
                                (to.q_count < 1 ? 1 : to.q_count) * a.pitch_q * 2);
         aim_block();
     };
-    if constexpr (kPAcross) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            op[i] = (uint32_t)(wave * 8 + lane / 32) * pitch_p +
-                    ((lane % 32) ^ (lane / 32 * 2) ^ (i * 4) ^ (wave % 2 * 8)) * 16;
-    }
-    if constexpr (kQAcross) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            oq[i] = (uint32_t)(wave * 8 + lane / 32) * pitch_q +
-                    ((lane % 32) ^ (lane / 32 * 2) ^ (i * 4) ^ (wave % 2 * 8)) * 16;
+    for (int i = 0; i < 4; ++i) {
+        const int c = (lane % 8) ^ (lane / 16) ^ (i % 2 * 4);
+        op[i] = (uint32_t)(lane / 8) * pitch_p + c * 16;
+        oq[i] = (uint32_t)(wave * 8 * kBigCopies + lane / 8) * pitch_q + c * 16;
+        if constexpr (kPAcross)
+            op[i] = (uint32_t)(wave * 2 * kBigCopies + lane / 32) * pitch_p +
+                    ((lane % 32) ^ (lane / 32 * 2) ^ (i % 2 * 4) ^
+                     ((wave * kBigCopies / 4 + i / 2) % 2 * 8)) * 16;
+        if constexpr (kQAcross)
+            oq[i] = (uint32_t)(wave * 2 * kBigCopies + lane / 32) * pitch_q +
+                    ((lane % 32) ^ (lane / 32 * 2) ^ (i % 2 * 4) ^
+                     ((wave * kBigCopies / 4 + i / 2) % 2 * 8)) * 16;
     }
     // behind the last tile the copies repeat its last block
     const auto advance = [&]() {
-        if (++fb < to.blocks) {
-            aim_block();
-            return;
-        }
+        if (uniform(++fb < to.blocks)) return aim_block();
         int next = ft + 1;
         BigTile t{};
         for (; next < share.count; ++next) {
             t = tile_at(next);
             if (!kWeights || t.blocks > 0) break;
         }
-        if (next < share.count) {
+        if (uniform(next < share.count)) {
             ft = next;
             to = t;
             fb = 0;
             aim();
         } else {
             fb = to.blocks - 1;
+            aim_block();
+        }
+    };
+    // The same for a block that is neither its tile's first nor its last, without a branch:
+    // nothing changes but where it begins.  on: 1, or 0 to stay.
+    const auto step = [&](int on) {
+        fb += on;
+        if constexpr (kPAcross) {
+            pb += (int64_t)(on * kDepth) * a.pitch_p;
+            pbuf = buffer_rsrc(const_cast<uint16_t*>(pb), (kDepth * a.pitch_p - to.p0) * 2);
+        }
+        if constexpr (kQAcross) {
+            qb += (int64_t)(on * kDepth) * a.pitch_q;
+            qbuf = buffer_rsrc(const_cast<uint16_t*>(qb), (kDepth * a.pitch_q - (int)to.q0) * 2);
         }
     };
     const auto fetch_p = [&](uint32_t at, int i) {
-        to_lds(pbuf, op[i % 2] + (uint32_t)i * (kPAcross ? 2 : 8) * pitch_p,
-               kPAcross ? 0 : fb * 128, s_mem + at + wave * 4096 + i * 1024);
+        to_lds(pbuf, op[kPAcross ? i % 2 + i / 4 * 2 : i % 2] + (uint32_t)i * (kPAcross ? 2 : 8) * pitch_p,
+               kPAcross ? 0 : fb * 128, s_mem + at + (wave * kBigCopies + i) * 1024);
     };
     const auto fetch_q = [&](uint32_t at, int i) {
-        to_lds(qbuf, oq[i % 2] + (uint32_t)i * (kQAcross ? 2 : 8) * pitch_q,
-               kQAcross ? 0 : fb * 128, s_mem + at + wave * 4096 + i * 1024);
+        to_lds(qbuf, oq[kQAcross ? i % 2 + i / 4 * 2 : i % 2] + (uint32_t)i * (kQAcross ? 2 : 8) * pitch_q,
+               kQAcross ? 0 : fb * 128, s_mem + at + (wave * kBigCopies + i) * 1024);
     };
 
     // Reads: lane's column of P (Q) is r = lane % 16 of a tile of 16, its c's are 8 g on,
@@ -485,7 +536,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
     const int r = lane % 16, g = lane / 16;
     const int along = r * 128 + (g ^ (r / 2)) * 16;
     const int fold = r / 4 + g % 2 * 4, across = (8 * g + r / 4) * 512 + r % 4 * 8;
-    const int across_p = across + ((wp * 8) ^ fold) * 32, across_q = across + ((wq * 4) ^ fold) * 32;
+    const int across_p = across + ((wp * 8) ^ fold) * 32, across_q = across + ((wq * kBigQTiles) ^ fold) * 32;
     const auto ptile = [&](uint32_t at, int i, int h) {
         if constexpr (kPAcross)
             return lds_across(s_mem + at + (across_p ^ (i * 32)) + h * 16384, 2048);
@@ -496,7 +547,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
         if constexpr (kQAcross)
             return lds_across(s_mem + at + (across_q ^ (j * 32)) + h * 16384, 2048);
         else
-            return lds16(s_mem + at + wq * 8192 + j * 2048 + (along ^ (h * 64)));
+            return lds16(s_mem + at + (wq * kBigQTiles + j) * 2048 + (along ^ (h * 64)));
     };
 
     // the first tile with a block
@@ -509,72 +560,83 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
     // places of this, the next and the over-next block
     uint32_t p_at[3] = {0, kOperandBytes, 2 * kOperandBytes};
     uint32_t q_at[2] = {kQAt, kQAt + kOperandBytes};
-    f32x4 acc[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    bf16x8 p[3][2], q[2][4];
+    f32x4 acc[8][kBigQTiles];
+    bf16x8 p[4][2], q[2][kBigQTiles];
     if (any) {
         aim();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kBigCopies; ++i) {
             fetch_p(p_at[0], i);
             fetch_q(q_at[0], i);
+        }
+        advance();
+#pragma unroll
+        for (int i = 0; i < kBigCopies; ++i) {
+            fetch_p(p_at[1], i);
+            fetch_q(q_at[1], i);
         }
         meet<0, 0>();
         advance();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            fetch_p(p_at[1], i);
-            fetch_q(q_at[1], i);
-        }
-#pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[h][j] = qtile(q_at[0], j, h);
+            for (int j = 0; j < kBigQTiles; ++j) q[h][j] = qtile(q_at[0], j, h);
             p[0][h] = ptile(p_at[0], 0, h);
+            p[1][h] = ptile(p_at[0], 1, h);
         }
     }
 
-    // One block: eight P tiles, eight MFMAs each.  P is read two tiles ahead.  Two
-    // meetings: at i = 1 every wavefront has its Q in registers, and their place takes
-    // Q of the block two ahead; at i = 6 every wavefront has read its P and the next
-    // block has arrived (all but the eight copies of the one after it), whose first
-    // reads follow under the MFMAs left.  A wavefront without any Q copies and meets
-    // only.
-    const auto block = [&](auto busy) {
-        constexpr int kReads = kPAcross ? 4 : 2;    // LDS reads of a tile of P
-        const auto read_p = [&](uint32_t at, int i, int to_reg) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) p[to_reg][h] = ptile(at, i, h);
+    // One block: eight P tiles i, sixteen MFMAs n each.  There is one wavefront on a SIMD:
+    // what else it has to issue goes between the MFMAs, a little at a time.  P is read
+    // two tiles ahead.  The copies of the block two ahead go out at an even pace, two a
+    // row, P's and then Q's (all sixteen in rows 0 to 5: 7 % slower where the operands do
+    // not fit the last-level cache, in rows 0 to 3: 18 %).  Two meetings: at i = 1 every
+    // wavefront has its Q in registers, and their place may take the next copies; at i = 6
+    // every wavefront has read its P and the next block has arrived (all but the twelve
+    // copies that this block has sent out so far).  The last two rows go by columns, so
+    // that Q of the next block can replace this one's over 32 MFMAs, each tile after its
+    // last use.
+    // A tile's first block begins from zero, and finds its next block there already: it
+    // was waited for ahead of the last tile's stores, which need not end before.
+    const auto block = [&](auto first) {
+        const auto add = [&](int i, int h, int j) {
+            const bool zero = first.value && h == 0;
+            acc[i][j] = mfma_bf16(p[i % 4][h], q[h][j], zero ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j]);
         };
+        constexpr int kReads = kPAcross ? 4 : 2;    // LDS reads of a tile of P
+        const bool inner = uniform(fb + 2 < to.blocks);      // the copies go on within their tile
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (busy.value) {
-                if (i == 0) read_p(p_at[0], 1, 1);
-                // the reads of P tile 2 may be under way, not Q's
-                if (i == 1) meet<63, kReads>();
-                if (i < 6) read_p(p_at[0], i + 2, (i + 2) % 3);
-            } else {
-                if (i == 1) meet<63, 0>();
+        for (int i = 0; i < 6; ++i) {
+            // the reads of P tile 2 may be under way, not Q's
+            if (i == 1) meet<63, kReads>();
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+                const int h = n / 8, j = n % 8;
+                __builtin_amdgcn_sched_barrier(0);
+                add(i, h, j);
+                __builtin_amdgcn_sched_barrier(0);
+                if (n == 1 || n == 4) p[(i + 2) % 4][n / 4] = ptile(p_at[0], i + 2, n / 4);
+                if (n % 8 == 6 && i < 4) fetch_p(p_at[2], 2 * i + n / 8);
+                if (n % 8 == 6 && i >= 4) fetch_q(q_at[0], 2 * i - 8 + n / 8);
             }
-            if (i < 4) fetch_p(p_at[2], i);
-            if (i >= 2 && i < 6) fetch_q(q_at[0], i - 2);
-            if (i == 6) meet<8, 0>();
-            if (i == 7) read_p(p_at[1], 0, 0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (busy.value) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        acc[i][j] = mfma_bf16(p[i % 3][h], q[h][j], acc[i][j]);
-                    }
-                    if (i == 7) q[h][j] = qtile(q_at[1], j, h);
-                }
         }
-        if constexpr (busy.value) __builtin_amdgcn_sched_barrier(0);
+        meet<first.value ? 63 : 12, 0>();
+#pragma unroll
+        for (int n = 0; n < 32; ++n) {
+            const int j = n / 4, h = n / 2 % 2, i = 6 + n % 2;
+            __builtin_amdgcn_sched_barrier(0);
+            add(i, h, j);
+            __builtin_amdgcn_sched_barrier(0);
+            if (n == 1 || n == 4) p[0][n / 4] = ptile(p_at[1], 0, n / 4);
+            if (n == 8 || n == 12) p[1][n / 4 - 2] = ptile(p_at[1], 1, n / 4 - 2);
+            if (n % 8 == 6) fetch_q(q_at[0], 4 + n / 8);
+            if (n == 31) step(inner);
+            if (n >= 5 && n % 2 == 1) q[n / 2 % 2][n / 4 - 1] = qtile(q_at[1], n / 4 - 1, n / 2 % 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) q[h][7] = qtile(q_at[1], 7, h);
+        if (!inner) advance();
         const uint32_t p0 = p_at[0], q0 = q_at[0];
         p_at[0] = p_at[1];
         p_at[1] = p_at[2];
@@ -585,27 +647,39 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
 
     for (int ti = 0; ti < share.count; ++ti) {
         const BigTile t = tile_at(ti);
-        const bool busy = wq * 64 < t.q_count;
-        for (int b = 0; b < t.blocks; ++b) {
-            advance();
-            if (busy)
-                block(std::true_type{});
-            else
-                block(std::false_type{});
+        if (kWeights && t.blocks == 0) {      // an expert without rows
+            const int vecs = (a.W - t.p0 < kBig ? a.W - t.p0 : kBig) / 8;
+            for (int i = (int)threadIdx.x; i < t.q_count * (kBig / 8); i += kBigThreads) {
+                const int c = i % (kBig / 8);
+                if (c >= vecs) continue;
+                const int64_t at =
+                    ((int64_t)t.e * a.V + t.q0 + i / (kBig / 8)) * a.W + t.p0 + c * 8;
+                u32x4* out = reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(a.out) +
+                                                      at * (WIDE ? 4 : 2));
+                out[0] = u32x4{0, 0, 0, 0};
+                if (WIDE) out[1] = u32x4{0, 0, 0, 0};
+            }
+            continue;
         }
-        if (busy) {
-            // (opaque: addresses made from them are not worth registers in the loop)
+        block(std::true_type{});
+        for (int b = 1; b < t.blocks; ++b) block(std::false_type{});
+        wait_vm();    // the next tile's first two blocks
+        {
+            // (opaque: addresses made from them are not worth registers in the loop.  The
+            // empty statements below keep the results in the accumulation registers until
+            // their turn: all of them at once do not fit the others.)
             int row = lane % 16, group = lane / 16;
             asm volatile("" : "+v"(row), "+v"(group));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int qi = wq * 64 + j * 16 + row;
+            for (int j = 0; j < kBigQTiles; ++j) {
+                const int qi = (wq * kBigQTiles + j) * 16 + row;
                 const int64_t qrow = t.q0 + qi;
                 const bool in = qi < t.q_count;
                 // A lane has columns 4 group .. 4 group + 3 of each 16: two neighbouring
                 // tiles' halves change hands, so that it has 8 of one of them.
                 const auto store8 = [&](const f32x4& v, const f32x4& w, uint16_t* out, int first,
                                         int end) {
+                    __builtin_amdgcn_sched_barrier(0);   // few results at a time
                     const u32x2 lo = __builtin_amdgcn_permlane16_swap(
                         bf16_pack(v[0], v[1]), bf16_pack(w[0], w[1]), false, false);
                     const u32x2 hi = __builtin_amdgcn_permlane16_swap(
@@ -619,42 +693,45 @@ __global__ __launch_bounds__(kBigThreads, 2) void bf16_big_kernel(Bf16Args a) {
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
                         const int first = t.p0 + wp * 64 + i * 16;
+                        asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i + 1][j]),
+                                     "+a"(acc[i + 4][j]), "+a"(acc[i + 5][j]));
                         if (a.pre) {
                             uint16_t* pre = a.pre + qrow * a.W;
                             store8(acc[i][j], acc[i + 1][j], pre, first, F);
                             store8(acc[i + 4][j], acc[i + 5][j], pre + F, first, F);
                         }
+                        f32x4 h[2];
 #pragma unroll
-                        for (int k = i; k < i + 2; ++k)
+                        for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                acc[k][j][v] *= sigmoid(acc[k][j][v]) * acc[k + 4][j][v];
-                        store8(acc[i][j], acc[i + 1][j],
-                               reinterpret_cast<uint16_t*>(a.out) + qrow * F, first, F);
+                            for (int v = 0; v < 4; ++v) {
+                                const float gate = acc[i + k][j][v];
+                                h[k][v] = gate * sigmoid(gate) * acc[i + k + 4][j][v];
+                            }
+                        store8(h[0], h[1], reinterpret_cast<uint16_t*>(a.out) + qrow * F, first, F);
                     }
                 } else {
                     const int64_t at = (kWeights ? (int64_t)t.e * a.V + qrow : qrow) * a.W;
                     const int first = t.p0 + wp * 128;
-                    if (kWeights && a.wide) {
+                    if constexpr (WIDE) {
                         float* out = reinterpret_cast<float*>(a.out) + at;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
+                            asm volatile("" : "+a"(acc[i][j]));
                             const int c = first + i * 16 + group * 4;
                             if (in && c < a.W) *reinterpret_cast<f32x4*>(out + c) = acc[i][j];
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 8; i += 2)
+                        for (int i = 0; i < 8; i += 2) {
+                            asm volatile("" : "+a"(acc[i][j]), "+a"(acc[i + 1][j]));
                             store8(acc[i][j], acc[i + 1][j], reinterpret_cast<uint16_t*>(a.out) + at,
                                    first + i * 16, a.W);
+                        }
                     }
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     wait_vm();   // no copy may reach the LDS after the workgroup's end
 }
@@ -777,7 +854,7 @@ int launch_small(Bf16Args& a, hipStream_t stream) {
 
 // A workgroup a CU, or, for fewer tiles, one each, in whole eights for the XCDs
 // that share them out.
-template <int MODE>
+template <int MODE, bool WIDE>
 int launch_big(Bf16Args& a, hipStream_t stream) {
     a.tiles_w = (int32_t)(MODE == kGate ? ceil_div(a.W / 2, kBig / 2) : ceil_div(a.W, kBig));
     if (MODE == kWeightBack) {
@@ -791,7 +868,7 @@ int launch_big(Bf16Args& a, hipStream_t stream) {
         return EP_ERR_INVALID_ARG;
     }
     clear_hip_error();
-    hipLaunchKernelGGL(bf16_big_kernel<MODE>,
+    hipLaunchKernelGGL((bf16_big_kernel<MODE, WIDE>),
                        dim3((unsigned)(a.tiles < kBigGrid ? ceil_div(a.tiles, 8) * 8 : kBigGrid)),
                        dim3(kBigThreads), 0, stream, a);
     EP_HIP_CHECK(hipGetLastError());
@@ -800,7 +877,9 @@ int launch_big(Bf16Args& a, hipStream_t stream) {
 
 template <int MODE>
 int launch(Bf16Args& a, hipStream_t stream) {
-    if (a.M >= (int64_t)a.G * 128 && a.splits == 1) return launch_big<MODE>(a, stream);
+    if (a.M >= (int64_t)a.G * 128 && a.splits == 1)
+        return a.wide ? launch_big<MODE, MODE == kWeightBack>(a, stream)
+                      : launch_big<MODE, false>(a, stream);
     return launch_small<MODE>(a, stream);
 }
 

@@ -20,41 +20,50 @@ struct RowTile {
 
 __device__ inline int64_t clamp_row(int64_t r, int64_t M) { return r < 0 ? 0 : r > M ? M : r; }
 
+// A step of find_tile: lane l has the first row `lo` and the `n` rows of group g0 + l.
+// Whether `tile` is one of theirs (or one that overlapping groups leave out: r->g is
+// -1 then), *before* the tiles of the groups before g0, which gets theirs added.
+__device__ inline bool find_in(int64_t lo, int64_t n, int g0, int64_t* before, int64_t tile, int bm,
+                               RowTile* r) {
+    const int lane = lane_id();
+    const int t = (int)((n + bm - 1) / bm);
+    int sum = t;   // inclusive scan: at most M < 2^31 tiles where the offsets are in order
+#pragma unroll
+    for (int o = 1; o < kWave; o *= 2) {
+        const int up = __shfl_up(sum, o);
+        sum += lane >= o ? up : 0;
+    }
+    const uint64_t here = __ballot(tile < *before + sum);
+    if (here) {
+        const int l = __builtin_ctzll(here);
+        const int in = (int)(tile - *before) - (bcast(sum, l) - bcast(t, l));
+        // overlapping groups can wrap the sum: such a tile is left out
+        if (in < 0 || in >= bcast(t, l)) return true;
+        r->g = g0 + l;
+        r->first = (int64_t)bcast((int32_t)lo, l) + (int64_t)in * bm;
+        const int64_t left = (int64_t)bcast((int32_t)n, l) - (int64_t)in * bm;
+        r->count = (int)(left < bm ? left : bm);
+        return true;
+    }
+    *before += bcast(sum, kWave - 1);
+    return false;
+}
+
 // Called by whole wavefronts: lane l looks at group g0 + l, 64 groups a step.
 // Offsets outside [0, M] or decreasing are clamped, so that a tile's rows are
 // always rows of the buffers (check_groups reports them).
 __device__ inline RowTile find_tile(const int32_t* off, int G, int64_t M, int64_t tile, int bm) {
     RowTile r{-1, 0, 0};
-    const int lane = lane_id();
     int64_t before = 0;   // tiles of the groups before g0
     for (int g0 = 0; g0 < G; g0 += kWave) {
-        const int g = g0 + lane;
+        const int g = g0 + lane_id();
         int64_t lo = 0, n = 0;
         if (g < G) {
             lo = clamp_row(off[g], M);
             n = clamp_row(off[g + 1], M) - lo;
             n = n < 0 ? 0 : n;
         }
-        const int t = (int)((n + bm - 1) / bm);
-        int sum = t;   // inclusive scan: at most M < 2^31 tiles where the offsets are in order
-#pragma unroll
-        for (int o = 1; o < kWave; o *= 2) {
-            const int up = __shfl_up(sum, o);
-            sum += lane >= o ? up : 0;
-        }
-        const uint64_t here = __ballot(tile < before + sum);
-        if (here) {
-            const int l = __builtin_ctzll(here);
-            const int in = (int)(tile - before) - (bcast(sum, l) - bcast(t, l));
-            // overlapping groups can wrap the sum: such a tile is left out
-            if (in < 0 || in >= bcast(t, l)) return r;
-            r.g = g0 + l;
-            r.first = (int64_t)bcast((int32_t)lo, l) + (int64_t)in * bm;
-            const int64_t left = (int64_t)bcast((int32_t)n, l) - (int64_t)in * bm;
-            r.count = (int)(left < bm ? left : bm);
-            return r;
-        }
-        before += bcast(sum, kWave - 1);
+        if (find_in(lo, n, g0, &before, tile, bm, &r)) return r;
     }
     return r;
 }

@@ -114,8 +114,10 @@ def gate64(pre, off_pre):
     g, u = pre[:, :F], pre[:, F:]
     s = torch.sigmoid(g)
     h = g * s * u
-    # silu' <= 1.1; the sigmoid's exp, sum, quotient and two products: eight roundings
-    return h, 1.1 * off_pre[:, :F] * u.abs() + (g * s).abs() * off_pre[:, F:] + 1.1 * off_pre[:, :F] * off_pre[:, F:] + 8 * X.U32 * h.abs() * 4
+    # silu' <= 1.1; the sigmoid's exp, sum, quotient and two products: eight roundings.  A
+    # sigmoid below float's normal range (a gate below -87.3) is held in steps of 2^-149: the
+    # product is off by one of them times |g u|
+    return h, (g * u).abs() * 2.0 ** -149 + 1.1 * off_pre[:, :F] * u.abs() + (g * s).abs() * off_pre[:, F:] + 1.1 * off_pre[:, :F] * off_pre[:, F:] + 8 * X.U32 * h.abs() * 4
 
 
 @pytest.mark.parametrize("keep", [True, False])
@@ -170,6 +172,38 @@ def test_gate_up_backward(ep, sizes, F, K, first, behind, kind):
     again = torch.full_like(grad_pre, POISON)
     ep.ep_expert_gate_up_bf16_backward(c.rows, c.off, c.w, pre, d, again, None, None, c.st)
     assert torch.equal(again, grad_pre) and int(c.st) == 0
+
+
+# many rows an expert: tiles of one to several blocks, several tiles a workgroup, more
+# experts than lanes, experts without rows among large ones
+MANY = [([200], 8, 8), ([300], 264, 64), ([256], 256, 72), ([257, 255], 520, 128), ([513], 24, 136), ([150, 400], 512, 200),
+        ([9000], 2056, 72), ([5000, 0, 4500], 1096, 8), ([130 + i % 7 for i in range(70)], 264, 136), ([0, 3000, 0, 0, 10, 2000], 520, 328),
+        ([20000], 64, 64), ([140] * 40, 328, 1032)]
+
+
+@pytest.mark.parametrize("sizes,N,K", MANY)
+def test_many_rows(ep, sizes, N, K):
+    log(f"[bf16 many rows] {sizes[:6]} N={N} K={K}")
+    c = Case(sizes, N, K, 3, 5, whole=True, seed=11)
+    out, gr = torch.full((c.M, N), POISON, **BF), torch.full((c.M, K), POISON, **BF)
+    ep.ep_expert_product_bf16(c.rows, c.off, c.w, out, c.st)
+    c.check(out, *X.product64(c.rows, c.off, c.w), K, "out")
+    for kind in (torch.bfloat16, torch.float32):
+        gw = torch.full((c.G, N, K), POISON, dtype=kind, device="cuda")
+        gr.fill_(POISON)
+        ep.ep_expert_product_bf16_backward(c.rows, c.off, c.w, c.grad_out, gr, gw, c.st, c.workspace(ep))
+        c.check(gr, *X.product64(c.grad_out, c.off, c.w.transpose(1, 2)), N, "grad_rows")
+        c.close(gw, *X.weights64(c.rows, c.off, c.grad_out), max(sizes), "grad_w")
+    F = N // 2
+    if F % 8 == 0:
+        pre, h = torch.full((c.M, N), POISON, **BF), torch.full((c.M, F), POISON, **BF)
+        ep.ep_expert_gate_up_bf16(c.rows, c.off, c.w, pre, h, c.st)
+        want, mag = X.product64(c.rows, c.off, c.w)
+        c.check(pre, want, mag, K, "pre")
+        assert (h[~c.inside] == POISON).all()
+        act, off = gate64(want, torch.zeros_like(want))
+        assert_close(h[c.inside], act[c.inside], X.bf16_tol(act, off)[c.inside], "gated")
+    assert int(c.st) == 0
 
 
 def test_differences(ep):
