@@ -108,6 +108,11 @@ class ep_tensor_t(ctypes.Structure):
                 ("pad_", ctypes.c_int32)]
 
 
+class ep_tensor_list_t(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("units", ctypes.c_int64), ("sizes", ctypes.c_uint64),
+                ("count", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
 class ep_shape_t(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("R", ctypes.c_int32), ("k", ctypes.c_int32), ("fmt", ctypes.c_int32)]
@@ -190,11 +195,16 @@ def _load() -> ctypes.CDLL:
     L.ep_expert_gate_up_bf16_backward.argtypes = [i32, i64, i32, i32, i32, P, P, P, P, P, P, P, P,
                                                   P, P, sz, P]
     L.ep_expert_gate_up_bf16_backward.restype = ctypes.c_int
-    L.ep_grad_norm_workspace_bytes.argtypes = [i32]
+    TL = ctypes.POINTER(ep_tensor_list_t)
+    L.ep_tensor_table_bytes.argtypes = [i32]
+    L.ep_tensor_table_bytes.restype = sz
+    L.ep_tensor_table.argtypes = [i32, ctypes.POINTER(ep_tensor_t), P, TL]
+    L.ep_tensor_table.restype = ctypes.c_int
+    L.ep_grad_norm_workspace_bytes.argtypes = []
     L.ep_grad_norm_workspace_bytes.restype = sz
-    L.ep_grad_norm.argtypes = [i32, P, P, P, P, sz, P]
+    L.ep_grad_norm.argtypes = [TL, P, P, P, sz, P]
     L.ep_grad_norm.restype = ctypes.c_int
-    L.ep_grad_clip.argtypes = [i32, P, P, P, ctypes.c_double, P]
+    L.ep_grad_clip.argtypes = [TL, TL, P, ctypes.c_double, P]
     L.ep_grad_clip.restype = ctypes.c_int
     L.ep_ring_create.argtypes = [i32, i32, i32, i64]
     L.ep_ring_create.restype = P
@@ -393,16 +403,16 @@ def ep_combine_ll(s, y, topk_idx, topk_w, expert_slot, out, dev_status, stream=N
 # The calls below take their sizes from the tensors, so they also check each
 # tensor: type, shape, contiguity and the current device.
 
-_U8 = _I32 = _F32 = _BF16 = _E4M3 = None   # torch types, set at the first call
+_U8 = _I32 = _F32 = _F64 = _BF16 = _E4M3 = None   # torch types, set at the first call
 _device_now = _stream_of = None            # current device; its current stream's handle
 
 
 def _types() -> None:
     import torch
-    global _U8, _I32, _F32, _BF16, _E4M3, _device_now, _stream_of
+    global _U8, _I32, _F32, _F64, _BF16, _E4M3, _device_now, _stream_of
     _device_now, _stream_of = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
     _U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
-    _E4M3 = torch.float8_e4m3fn
+    _E4M3, _F64 = torch.float8_e4m3fn, torch.float64
 
 
 def _arg(name, t, dtype, shape_, device):
@@ -766,23 +776,24 @@ def ep_expert_gate_up_bf16_backward(rows, group_offset, w, pre, grad_out, grad_p
 
 
 class TensorList:
-    """Tensors of float32 and bfloat16 on one device, as ep_grad_norm and ep_grad_clip take
-    them.  Made once for gradients that keep their memory from step to step; it holds that
-    memory, so a tensor that is given other memory (``t.data = ...``) needs a new list.  Tensors
-    that overlap are refused."""
+    """Tensors of float32 and bfloat16 on the current device, as ep_grad_norm and ep_grad_clip
+    take them.  Made once for gradients that keep their memory from step to step (a table goes to
+    the GPU, and is waited for); it holds that memory, so a tensor that is given other memory
+    (``t.data = ...``) needs a new list.  Tensors that overlap are refused."""
 
     def __init__(self, tensors):
         import torch
         if _U8 is None:
             _types()
         keep = [t.detach() for t in tensors]
-        self.device = keep[0].get_device() if keep else None
+        self.device = _device_now()
         spans = []
         for i, t in enumerate(keep):
             if t.dtype is not _F32 and t.dtype is not _BF16:
                 raise ValueError(f"tensor {i} must be float32 or bfloat16, is {t.dtype}")
-            if t.get_device() != self.device or self.device < 0:
-                raise ValueError(f"tensor {i} must be on one GPU with the others, is on {t.device}")
+            if t.get_device() != self.device:
+                raise ValueError(f"tensor {i} must be on the current device ({self.device}), is "
+                                 f"on {t.device}")
             if not t.is_contiguous():
                 raise ValueError(f"tensor {i} must be contiguous")
             if t.numel():
@@ -791,58 +802,65 @@ class TensorList:
         for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError(f"tensors {i} and {j} overlap")
-        self.tensors = keep
-        self.count = len(keep)
-        self.array = (ep_tensor_t * max(1, self.count))(
+        count = len(keep)
+        array = (ep_tensor_t * max(1, count))(
             *[ep_tensor_t(t.data_ptr() if t.numel() else None, t.numel(),
-                          EP_F32 if t.dtype is torch.float32 else EP_BF16, 0) for t in keep])
+                          EP_F32 if t.dtype is _F32 else EP_BF16, 0) for t in keep])
+        table = torch.empty(int(lib.ep_tensor_table_bytes(count)), dtype=torch.uint8)
+        self.c = ep_tensor_list_t()
+        _check(lib.ep_tensor_table(count, array, table.data_ptr(), ctypes.byref(self.c)),
+               "ep_tensor_table")
+        self.tensors = keep
+        self.table = table.to(torch.device("cuda", self.device))
+        self.c.table = self.table.data_ptr()
 
-    def on(self, device, name) -> None:
-        if self.device is not None and self.device != device:
-            raise ValueError(f"{name} must be on the current device ({device}), are on "
-                             f"{self.device}")
+    def __len__(self) -> int:
+        return len(self.tensors)
 
 
-def _tensor_list(tensors, device, name) -> TensorList:
+def _tensor_list(tensors, device, stream, name) -> TensorList:
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
-    tensors.on(device, name)
+        if stream is not None:      # its table outlives the call there
+            tensors.table.record_stream(stream)
+    if tensors.device != device:
+        raise ValueError(f"{name} must be on the current device ({device}), are on "
+                         f"{tensors.device}")
     return tensors
 
 
-def ep_grad_norm_workspace_bytes(tensors) -> int:
-    """Of a TensorList, a sequence of tensors or their number."""
-    count = (tensors if isinstance(tensors, int) else
-             tensors.count if isinstance(tensors, TensorList) else len(tensors))
-    return int(lib.ep_grad_norm_workspace_bytes(count))
+def ep_grad_norm_workspace_bytes(tensors=None) -> int:
+    """The same for any list."""
+    return int(lib.ep_grad_norm_workspace_bytes())
 
 
 def _sum_squares(t, device):
-    import torch
-    return _arg("sum_squares", _need("sum_squares", t), torch.float64, (1,), device)
+    return _arg("sum_squares", _need("sum_squares", t), _F64, (1,), device)
 
 
 def ep_grad_norm(tensors, sum_squares, norm, workspace, stream=None) -> None:
-    """tensors: a TensorList, or a sequence of tensors (a list made anew for the call)."""
+    """tensors: a TensorList, or a sequence of tensors, for which one is made (not under graph
+    capture: it waits for its table)."""
     device, st_ = _call_device(stream)
-    tensors = _tensor_list(tensors, device, "tensors")
-    ws, ws_bytes = _workspace(workspace, device, ep_grad_norm_workspace_bytes(tensors))
-    st = lib.ep_grad_norm(tensors.count, tensors.array, _sum_squares(sum_squares, device),
+    tensors = _tensor_list(tensors, device, stream, "tensors")
+    ws, ws_bytes = _workspace(workspace, device, ep_grad_norm_workspace_bytes())
+    st = lib.ep_grad_norm(ctypes.byref(tensors.c), _sum_squares(sum_squares, device),
                           _arg("norm", norm, _F32, (1,), device), ws, ws_bytes, st_)
     _check(st, "ep_grad_norm")
 
 
 def ep_grad_clip(tensors, sum_squares, max_norm, into=None, stream=None) -> None:
+    """tensors and into as at ep_grad_norm."""
     device, st_ = _call_device(stream)
-    tensors = _tensor_list(tensors, device, "tensors")
-    into_array = None
+    tensors = _tensor_list(tensors, device, stream, "tensors")
+    into_c = None
     if into is not None:
-        into = _tensor_list(into, device, "into")
-        if into.count != tensors.count:
-            raise ValueError(f"into must have {tensors.count} tensors, has {into.count}")
-        into_array = into.array
-    st = lib.ep_grad_clip(tensors.count, tensors.array, into_array,
-                          _sum_squares(sum_squares, device), max_norm, st_)
+        into = _tensor_list(into, device, stream, "into")
+        if len(into) != len(tensors):
+            raise ValueError(f"into must have {len(tensors)} tensors, has {len(into)}")
+        into_c = ctypes.byref(into.c)
+    st = lib.ep_grad_clip(ctypes.byref(tensors.c), into_c, _sum_squares(sum_squares, device),
+                          max_norm, st_)
     _check(st, "ep_grad_clip")
 
 

@@ -1,17 +1,19 @@
 // ep_grad_norm.hip — the norm of all gradients together, and their clipping.
 //
-// The tensors of a call come as a host table, which goes to the kernels by value
-// (kTable tensors a launch).  A tensor is cut into units of kUnit threads' loads;
-// a workgroup takes one run of the launch's units and looks its first tensor up
-// once.  Loads are 16 bytes from the first aligned element on; the elements
-// before it belong to the first unit.
+// The tensors come as a table in device memory, made once on the host.  A tensor
+// is cut into units of kUnit elements (one pass of a workgroup's loads), which the
+// workgroups take in turn, a few at a time.  Units begin on a 128-byte line (a line
+// written in two parts costs as two); the elements before a tensor's first line
+// belong to its first unit.
 //
 // The norm: squares and their sums in double (a float's square leaves float's
 // range from 1.8e19 up and, towards zero, 1e-19 down); a partial sum a workgroup;
-// the last workgroup of the last launch adds them in their order.
+// the last workgroup that ends adds them in their order.
 //
 // The clip: v * m * 2^e with max_norm / norm = m * 2^e, so a ratio below float's
 // range still scales what float holds.
+
+#include <string.h>
 
 #include "ep_rows8.h"
 
@@ -19,93 +21,119 @@ namespace ep {
 
 constexpr int kGradThreads = 1024;
 constexpr int kGradGrid = 512;            // two workgroups a CU
-constexpr int kTable = 128;               // tensors of a launch: its table is 3.6 KB of arguments
 constexpr int kUnitVecs = 2;              // groups of 8 elements a thread
 constexpr int kUnit = kGradThreads * 8 * kUnitVecs;
-constexpr int64_t kMaxTensor = (int64_t)1 << 38;   // elements: a launch's units fit 32 bits
-static_assert((kMaxTensor / kUnit + 1) * kTable < ((int64_t)1 << 32), "units fit 32 bits");
+constexpr int kHeld = 1024;               // tensors whose entries a workgroup holds in LDS
+constexpr int kMostChunk = 2;             // units that a workgroup takes at a time
+constexpr int64_t kMaxTensor = (int64_t)1 << 38;   // elements
+constexpr int64_t kMaxUnits = (int64_t)1 << 31;
 
-struct GradTable {
-    const void* src[kTable];    // bit 0: float (an address of either type has it clear)
-    void* dst[kTable];          // clip only; bit 0 as src's
-    int64_t n[kTable];
-    uint32_t first[kTable + 1]; // first unit of each tensor
-    int32_t count;
+// One tensor of the table; the entry behind the last one has `first` alone.
+struct GradEntry {
+    uint64_t data;      // bit 0: float (an address of either type has it clear)
+    int64_t n;
+    uint32_t first;     // its first unit; without elements it has none
+    uint32_t pad;
+    uint64_t pad2;
 };
+static_assert(sizeof(GradEntry) == 32, "entries stay 16-byte aligned");
 
 struct GradArgs {
-    GradTable t;
-    double* partial;            // norm: this launch's partial sums
-    const double* partials;     // norm, last launch: all of them
+    const GradEntry* src;
+    const GradEntry* dst;       // clip
+    double* partial;            // norm: a partial sum a workgroup
     double* sum_squares;
     float* norm;
-    uint32_t* ticket;           // norm, last launch: workgroups that are done
+    uint32_t* ticket;           // norm: workgroups that are done
     double max_norm;            // clip
     uint32_t units;
-    int32_t n_partials;         // norm: 0 in all launches but the last
+    int32_t count, chunk;
     bool in_place;              // clip
 };
 
-// Elements before the first 16-byte boundary.
-__host__ __device__ inline int64_t head_of(uintptr_t p, int64_t n, bool wide) {
-    const int64_t h = (int64_t)((16 - (p & 15)) & 15) / (wide ? 4 : 2);
+// Elements before the first line.
+__host__ __device__ inline int64_t head_of(uint64_t p, int64_t n, bool wide) {
+    const int64_t h = (int64_t)((128 - (p & 127)) & 127) / (wide ? 4 : 2);
     return h < n ? h : n;
 }
 
-__device__ inline float load1(const void* p, int64_t i, bool wide) {
-    return wide ? reinterpret_cast<const float*>(p)[i]
-                : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << 16);
+__device__ inline float load1(uint64_t p, int64_t i) {
+    return p & 1 ? reinterpret_cast<const float*>(p & ~1ull)[i]
+                 : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << 16);
 }
 
 // Eight elements from an aligned address.
-__device__ inline void load8(const void* p, int64_t i, bool wide, float* f) {
-    if (wide) {
-        const f32x4* q = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i);
-        const f32x4 a = __builtin_nontemporal_load(q), b = __builtin_nontemporal_load(q + 1);
+__device__ inline void load8(uint64_t p, int64_t i, float* f) {
+    if (p & 1) {
+        const f32x4* q = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p & ~1ull) + i);
+        const f32x4 a = q[0], b = q[1];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f[j] = a[j];
             f[4 + j] = b[j];
         }
     } else {
-        unpack8(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-                    reinterpret_cast<const uint16_t*>(p) + i)),
-                f);
+        unpack8(*reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p) + i), f);
     }
 }
 
-// Walks a workgroup's run of units.  `eight(tensor, i)` gets the first of eight
-// aligned elements, `one(tensor, i)` a single one.
-template <typename EIGHT, typename ONE>
+// Walks a workgroup's units.  `eight(from, to, i)` gets a tensor's addresses and the
+// first of eight aligned elements, `one(from, to, i)` a single one.  The clip goes
+// through them from the end: what the norm read last is in cache first.
+template <bool CLIP, typename EIGHT, typename ONE>
 __device__ inline void walk(const GradArgs& a, EIGHT eight, ONE one) {
-    const uint32_t per = a.units / gridDim.x, extra = a.units % gridDim.x, b = blockIdx.x;
-    uint32_t u = b * per + (b < extra ? b : extra);
-    const uint32_t end = u + per + (b < extra);
-    if (u == end) return;
-    int lo = 0, hi = a.t.count - 1;     // the last tensor whose first unit is not behind u
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.t.first[mid] <= u)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
+    __shared__ uint32_t s_first[kHeld + 1];
+    __shared__ uint64_t s_from[kHeld], s_to[CLIP ? kHeld : 1];
+    __shared__ int64_t s_n[kHeld];
+    const bool held = a.count <= kHeld;
     const int tid = (int)threadIdx.x;
-    for (int t = lo; u < end; ++u) {
-        if (u >= a.t.first[t + 1]) ++t;     // every tensor of the table has a unit
-        const uintptr_t p = (uintptr_t)a.t.src[t];
-        const bool wide = p & 1;
-        const int64_t n = a.t.n[t], head = head_of(p & ~(uintptr_t)1, n, wide);
-        const uint32_t in = u - a.t.first[t];
-        if (in == 0 && tid < head) one(t, (int64_t)tid);
-        const int64_t at = head + (int64_t)in * kUnit;
-#pragma unroll
-        for (int v = 0; v < kUnitVecs; ++v) {
-            const int64_t i = at + (int64_t)(v * kGradThreads + tid) * 8;
-            if (i + 8 <= n)
-                eight(t, i);
+    for (int i = tid; held && i <= a.count; i += kGradThreads) {
+        const GradEntry e = a.src[i];
+        s_first[i] = e.first;
+        if (i < a.count) {
+            s_from[i] = e.data;
+            s_n[i] = e.n;
+            if (CLIP) s_to[i] = a.dst[i].data;
+        }
+    }
+    __syncthreads();
+    const auto first = [&](int i) { return held ? s_first[i] : a.src[i].first; };
+    const uint32_t chunks = (a.units + a.chunk - 1) / a.chunk;
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        uint32_t u = (CLIP ? chunks - 1 - c : c) * a.chunk;
+        const uint32_t end = u + a.chunk < a.units ? u + a.chunk : a.units;
+        int t = 0;      // the last tensor whose first unit is not behind u
+        for (int hi = a.count - 1; t < hi;) {
+            const int mid = (t + hi + 1) / 2;
+            if (first(mid) <= u)
+                t = mid;
             else
-                for (int64_t j = i; j < n; ++j) one(t, j);
+                hi = mid - 1;
+        }
+        while (u < end) {
+            while (u >= first(t + 1)) ++t;
+            const uint64_t p = held ? s_from[t] : a.src[t].data;
+            const uint64_t d = !CLIP ? 0 : held ? s_to[t] : a.dst[t].data;
+            const int64_t n = held ? s_n[t] : a.src[t].n, head = head_of(p & ~1ull, n, p & 1);
+            const uint32_t at = first(t), stop = first(t + 1) < end ? first(t + 1) : end;
+            if (u == at && tid < head) one(p, d, (int64_t)tid);
+            for (; u < stop; ++u) {
+                const int64_t from = head + (int64_t)(u - at) * kUnit;
+                if (from + kUnit <= n) {
+#pragma unroll
+                    for (int v = 0; v < kUnitVecs; ++v)
+                        eight(p, d, from + (int64_t)(v * kGradThreads + tid) * 8);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < kUnitVecs; ++v) {
+                        const int64_t i = from + (int64_t)(v * kGradThreads + tid) * 8;
+                        if (i + 8 <= n)
+                            eight(p, d, i);
+                        else
+                            for (int64_t j = i; j < n; ++j) one(p, d, j);
+                    }
+                }
+            }
         }
     }
 }
@@ -128,34 +156,33 @@ __device__ inline double block_sum(double v) {
 __global__ __launch_bounds__(kGradThreads) void grad_norm_kernel(GradArgs a) {
     double sum = 0.0;
     const auto add = [&](float f) { sum = fma((double)f, (double)f, sum); };
-    walk(
+    walk<false>(
         a,
-        [&](int t, int64_t i) {
-            const uintptr_t p = (uintptr_t)a.t.src[t];
+        [&](uint64_t p, uint64_t, int64_t i) {
             float f[8];
-            load8((const void*)(p & ~(uintptr_t)1), i, p & 1, f);
+            load8(p, i, f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) add(f[q]);
         },
-        [&](int t, int64_t i) {
-            const uintptr_t p = (uintptr_t)a.t.src[t];
-            add(load1((const void*)(p & ~(uintptr_t)1), i, p & 1));
-        });
+        [&](uint64_t p, uint64_t, int64_t i) { add(load1(p, i)); });
     sum = block_sum(sum);
     __shared__ bool s_last;
     if (threadIdx.x == 0) {
+        // The partial sum goes past the XCD's L2 and is waited for before the ticket; the
+        // last one's loads go past it too.  (Fences would have every workgroup write its
+        // L2 back and clear it: 22 us in place of 16 for 40 MB in 100 tensors.)
         __hip_atomic_store(a.partial + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = false;
-        if (a.n_partials) {
-            s_last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL,
-                                            __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-        }
+        asm volatile("" ::: "memory");
+        wait_vm();
+        asm volatile("" ::: "memory");
+        s_last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 gridDim.x - 1;
     }
     __syncthreads();
     if (!s_last) return;
     sum = 0.0;
-    for (int i = (int)threadIdx.x; i < a.n_partials; i += kGradThreads)
-        sum += __hip_atomic_load(a.partials + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = (int)threadIdx.x; i < (int)gridDim.x; i += kGradThreads)
+        sum += __hip_atomic_load(a.partial + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     sum = block_sum(sum);
     if (threadIdx.x == 0) {
         *a.sum_squares = sum;
@@ -170,21 +197,19 @@ __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(GradArgs a) {
     if (!clip && a.in_place) return;
     int e = 0;
     const float m = clip ? (float)frexp(a.max_norm / norm, &e) : 1.0f;
-    walk(
+    walk<true>(
         a,
-        [&](int t, int64_t i) {
-            const uintptr_t p = (uintptr_t)a.t.src[t], d = (uintptr_t)a.t.dst[t];
+        [&](uint64_t p, uint64_t d, int64_t i) {
             float f[8];
-            load8((const void*)(p & ~(uintptr_t)1), i, p & 1, f);
+            load8(p, i, f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) f[q] = ldexpf(f[q] * m, e);
             if (d & 1) {
-                float* o = reinterpret_cast<float*>(d & ~(uintptr_t)1) + i;
+                float* o = reinterpret_cast<float*>(d & ~1ull) + i;
                 if (((uintptr_t)o & 15) == 0) {
-                    __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]},
-                                                reinterpret_cast<f32x4*>(o));
-                    __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]},
-                                                reinterpret_cast<f32x4*>(o) + 1);
+                    // (not streaming: the two halves of 32 bytes meet in cache)
+                    reinterpret_cast<f32x4*>(o)[0] = f32x4{f[0], f[1], f[2], f[3]};
+                    reinterpret_cast<f32x4*>(o)[1] = f32x4{f[4], f[5], f[6], f[7]};
                 } else {
 #pragma unroll
                     for (int q = 0; q < 8; ++q) o[q] = f[q];
@@ -200,54 +225,19 @@ __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(GradArgs a) {
                 }
             }
         },
-        [&](int t, int64_t i) {
-            const uintptr_t p = (uintptr_t)a.t.src[t], d = (uintptr_t)a.t.dst[t];
-            const float f = ldexpf(load1((const void*)(p & ~(uintptr_t)1), i, p & 1) * m, e);
+        [&](uint64_t p, uint64_t d, int64_t i) {
+            const float f = ldexpf(load1(p, i) * m, e);
             if (d & 1)
-                reinterpret_cast<float*>(d & ~(uintptr_t)1)[i] = f;
+                reinterpret_cast<float*>(d & ~1ull)[i] = f;
             else
                 reinterpret_cast<uint16_t*>(d)[i] = (uint16_t)bf16_pack(f, 0.0f);
         });
 }
 
-// A tensor of the table: its data may be NULL only where it has no elements.
-int check_tensor(const ep_tensor_t& t) {
-    if (t.n < 0 || t.n >= kMaxTensor) return EP_ERR_INVALID_ARG;
-    if (t.dtype != EP_BF16 && t.dtype != EP_F32) return EP_ERR_INVALID_ARG;
-    if (t.n > 0 && !t.data) return EP_ERR_INVALID_ARG;
-    if ((uintptr_t)t.data & (t.dtype == EP_F32 ? 3 : 1)) return EP_ERR_INVALID_ARG;
-    return EP_OK;
-}
-
-int check_tensors(int32_t count, const ep_tensor_t* t) {
-    if (count < 0 || (count > 0 && !t)) return EP_ERR_INVALID_ARG;
-    for (int32_t i = 0; i < count; ++i)
-        if (check_tensor(t[i]) != EP_OK) return EP_ERR_INVALID_ARG;
-    return EP_OK;
-}
-
-// Fills a launch's table from tensor *at on, and moves *at behind its last.
-void fill_table(GradArgs& a, int32_t count, const ep_tensor_t* src, const ep_tensor_t* dst,
-                int32_t* at) {
-    GradTable& t = a.t;
-    t.count = 0;
-    int64_t units = 0;
-    for (; *at < count && t.count < kTable; ++*at) {
-        const ep_tensor_t& s = src[*at];
-        if (s.n == 0) continue;
-        const bool wide = s.dtype == EP_F32;
-        const int64_t rest = s.n - head_of((uintptr_t)s.data, s.n, wide);
-        const int64_t mine = rest ? ceil_div(rest, kUnit) : 1;
-        t.src[t.count] = (const void*)((uintptr_t)s.data | (wide ? 1 : 0));
-        if (dst)
-            t.dst[t.count] =
-                (void*)((uintptr_t)dst[*at].data | (dst[*at].dtype == EP_F32 ? 1 : 0));
-        t.n[t.count] = s.n;
-        t.first[t.count++] = (uint32_t)units;
-        units += mine;
-    }
-    t.first[t.count] = (uint32_t)units;
-    a.units = (uint32_t)units;
+// Its data may be NULL only where a tensor has no elements.
+bool tensor_fits(const ep_tensor_t& t) {
+    return t.n >= 0 && t.n < kMaxTensor && (t.dtype == EP_BF16 || t.dtype == EP_F32) &&
+           (t.n == 0 || t.data) && ((uintptr_t)t.data & (t.dtype == EP_F32 ? 3 : 1)) == 0;
 }
 
 }  // namespace ep
@@ -256,67 +246,102 @@ using namespace ep;
 
 namespace {
 constexpr size_t kTicketBytes = 256;     // of the workspace, ahead of the partial sums
+
+int list_fits(const ep_tensor_list_t* l) {
+    return l && l->count >= 0 && l->units >= 0 && l->units < kMaxUnits &&
+           (l->units == 0 || (l->table && ((uintptr_t)l->table & 15) == 0));
 }
 
-extern "C" size_t ep_grad_norm_workspace_bytes(int32_t count) {
-    if (count < 0) return 0;
-    return kTicketBytes + (size_t)kGradGrid * 8 * (1 + (size_t)count / kTable);
+// Launch shape: a few turns of the workgroups where there is enough, so that none
+// has much more than the others.
+unsigned grad_grid(GradArgs& a) {
+    const int64_t chunk = a.units / (4 * kGradGrid);
+    a.chunk = (int32_t)(chunk < 1 ? 1 : chunk < kMostChunk ? chunk : kMostChunk);
+    return a.units < 1 ? 1u : a.units < (uint32_t)kGradGrid ? a.units : (uint32_t)kGradGrid;
+}
+}  // namespace
+
+extern "C" size_t ep_tensor_table_bytes(int32_t count) {
+    return count < 0 ? 0 : ((size_t)count + 1) * sizeof(GradEntry);
 }
 
-extern "C" int ep_grad_norm(int32_t count, const ep_tensor_t* tensors, double* sum_squares,
-                            float* norm, void* workspace, size_t workspace_bytes,
-                            hipStream_t stream) {
-    const int v = check_tensors(count, tensors);
-    if (v != EP_OK) return v;
-    if (!sum_squares || ((uintptr_t)sum_squares & 7) || ((uintptr_t)norm & 3) || !workspace ||
-        ((uintptr_t)workspace & 15) || workspace_bytes < ep_grad_norm_workspace_bytes(count))
+extern "C" int ep_tensor_table(int32_t count, const ep_tensor_t* tensors, void* table,
+                               ep_tensor_list_t* list) {
+    if (count < 0 || (count > 0 && !tensors) || !table || ((uintptr_t)table & 7) || !list)
         return EP_ERR_INVALID_ARG;
-    GradArgs a{};
-    a.ticket = reinterpret_cast<uint32_t*>(workspace);
-    double* const partials =
-        reinterpret_cast<double*>(reinterpret_cast<uint8_t*>(workspace) + kTicketBytes);
-    a.partials = partials;
-    a.sum_squares = sum_squares;
-    a.norm = norm;
-    int32_t left = 0;        // tensors with elements
-    for (int32_t i = 0; i < count; ++i) left += tensors[i].n > 0;
-    int32_t at = 0;
-    int64_t done = 0;
-    do {
-        fill_table(a, count, tensors, nullptr, &at);
-        left -= a.t.count;
-        // without a unit one workgroup still writes the sum, zero
-        const uint32_t grid =
-            a.units < (uint32_t)kGradGrid ? (a.units ? a.units : 1u) : (uint32_t)kGradGrid;
-        a.partial = partials + done;
-        done += grid;
-        a.n_partials = left == 0 ? (int32_t)done : 0;
-        clear_hip_error();
-        hipLaunchKernelGGL(grad_norm_kernel, dim3(grid), dim3(kGradThreads), 0, stream, a);
-        EP_HIP_CHECK(hipGetLastError());
-    } while (left > 0);
+    GradEntry* e = reinterpret_cast<GradEntry*>(table);
+    memset(e, 0, ep_tensor_table_bytes(count));
+    int64_t units = 0;
+    uint64_t sizes = 1469598103934665603ull;
+    for (int32_t i = 0; i < count; ++i) {
+        const ep_tensor_t& t = tensors[i];
+        if (!tensor_fits(t)) return EP_ERR_INVALID_ARG;
+        const bool wide = t.dtype == EP_F32;
+        e[i].data = (uint64_t)(uintptr_t)t.data | (wide ? 1 : 0);
+        e[i].n = t.n;
+        e[i].first = (uint32_t)units;
+        const int64_t rest = t.n - head_of((uint64_t)(uintptr_t)t.data, t.n, wide);
+        units += t.n == 0 ? 0 : rest ? ceil_div(rest, kUnit) : 1;
+        if (units >= kMaxUnits) {
+            record_error("tensor table: more than 2^31 units of elements");
+            return EP_ERR_INVALID_ARG;
+        }
+        sizes = (sizes ^ (uint64_t)t.n) * 1099511628211ull;
+        sizes ^= sizes >> 29;
+    }
+    e[count].first = (uint32_t)units;
+    list->table = nullptr;
+    list->units = units;
+    list->sizes = sizes;
+    list->count = count;
+    list->pad_ = 0;
     return EP_OK;
 }
 
-extern "C" int ep_grad_clip(int32_t count, const ep_tensor_t* tensors, const ep_tensor_t* into,
-                            const double* sum_squares, double max_norm, hipStream_t stream) {
-    int v = check_tensors(count, tensors);
-    if (v != EP_OK) return v;
-    if (into && (v = check_tensors(count, into)) != EP_OK) return v;
-    if (!sum_squares || ((uintptr_t)sum_squares & 7) || !(max_norm >= 0.0)) return EP_ERR_INVALID_ARG;
-    for (int32_t i = 0; into && i < count; ++i)
-        if (into[i].n != tensors[i].n) return EP_ERR_INVALID_ARG;
+extern "C" size_t ep_grad_norm_workspace_bytes(void) {
+    return kTicketBytes + (size_t)kGradGrid * sizeof(double);
+}
+
+extern "C" int ep_grad_norm(const ep_tensor_list_t* tensors, double* sum_squares, float* norm,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!list_fits(tensors)) return EP_ERR_INVALID_ARG;
+    if (!sum_squares || ((uintptr_t)sum_squares & 7) || ((uintptr_t)norm & 3) || !workspace ||
+        ((uintptr_t)workspace & 15) || workspace_bytes < ep_grad_norm_workspace_bytes())
+        return EP_ERR_INVALID_ARG;
     GradArgs a{};
+    a.src = reinterpret_cast<const GradEntry*>(tensors->table);
+    a.ticket = reinterpret_cast<uint32_t*>(workspace);
+    a.partial = reinterpret_cast<double*>(reinterpret_cast<uint8_t*>(workspace) + kTicketBytes);
+    a.sum_squares = sum_squares;
+    a.norm = norm;
+    a.units = (uint32_t)tensors->units;
+    a.count = tensors->count;
+    clear_hip_error();
+    // without a unit one workgroup still writes the sum, zero
+    hipLaunchKernelGGL(grad_norm_kernel, dim3(grad_grid(a)), dim3(kGradThreads), 0,
+                       stream, a);
+    EP_HIP_CHECK(hipGetLastError());
+    return EP_OK;
+}
+
+extern "C" int ep_grad_clip(const ep_tensor_list_t* tensors, const ep_tensor_list_t* into,
+                            const double* sum_squares, double max_norm, hipStream_t stream) {
+    if (!list_fits(tensors)) return EP_ERR_INVALID_ARG;
+    if (into && (!list_fits(into) || into->count != tensors->count || into->sizes != tensors->sizes))
+        return EP_ERR_INVALID_ARG;
+    if (!sum_squares || ((uintptr_t)sum_squares & 7) || !(max_norm >= 0.0)) return EP_ERR_INVALID_ARG;
+    if (tensors->units == 0) return EP_OK;
+    GradArgs a{};
+    a.src = reinterpret_cast<const GradEntry*>(tensors->table);
+    a.dst = into ? reinterpret_cast<const GradEntry*>(into->table) : a.src;
     a.sum_squares = const_cast<double*>(sum_squares);
     a.max_norm = max_norm;
     a.in_place = !into;
-    for (int32_t at = 0;;) {
-        fill_table(a, count, tensors, into ? into : tensors, &at);
-        if (a.units == 0) return EP_OK;
-        clear_hip_error();
-        hipLaunchKernelGGL(grad_clip_kernel,
-                           dim3(a.units < (uint32_t)kGradGrid ? a.units : (uint32_t)kGradGrid),
-                           dim3(kGradThreads), 0, stream, a);
-        EP_HIP_CHECK(hipGetLastError());
-    }
+    a.units = (uint32_t)tensors->units;
+    a.count = tensors->count;
+    clear_hip_error();
+    hipLaunchKernelGGL(grad_clip_kernel, dim3(grad_grid(a)), dim3(kGradThreads), 0,
+                       stream, a);
+    EP_HIP_CHECK(hipGetLastError());
+    return EP_OK;
 }

@@ -598,30 +598,45 @@ typedef struct ep_tensor {
     int32_t pad_;
 } ep_tensor_t;
 
-/* The sum of the squares of all elements of `count` tensors (a host array, read
- * before the call returns), and its root.
+/* A list of tensors, for calls on all of them: made once for tensors that keep
+ * their memory, or anew where they get other memory. */
+typedef struct ep_tensor_list {
+    const void* table;   /* device memory, 16-byte aligned: a copy of the table */
+    int64_t units;       /* set by ep_tensor_table, like what follows */
+    uint64_t sizes;
+    int32_t count;
+    int32_t pad_;
+} ep_tensor_list_t;
+
+/* Host only: fills `table`, ep_tensor_table_bytes(count) bytes of host memory, and
+ * *list, whose `table` the caller then sets to the address of the table's copy in
+ * device memory (on the device of the tensors).  A tensor may be empty, and count
+ * 0; tensors of a list must not overlap. */
+size_t ep_tensor_table_bytes(int32_t count);
+int ep_tensor_table(int32_t count, const ep_tensor_t* tensors, void* table,
+                    ep_tensor_list_t* list);
+
+/* The sum of the squares of all elements of a list, and its root.
  *   sum_squares double [1], on the device: of a group of GPUs, each its own
  *               tensors', to be added over them before ep_grad_clip
  *   norm        float [1], on the device, or NULL: the root
- *   workspace   ep_grad_norm_workspace_bytes(count) bytes, zero-filled once before
- *               its first use, left consistent by every call; calls that overlap in
+ *   workspace   ep_grad_norm_workspace_bytes() bytes, zero-filled once before its
+ *               first use, left consistent by every call; calls that overlap in
  *               time need one each
  * Squares and sums are double: any finite elements have a finite sum (norm is
- * infinite where the root is beyond float's range).  A tensor may be empty, and
- * count 0. */
-size_t ep_grad_norm_workspace_bytes(int32_t count);
-int ep_grad_norm(int32_t count, const ep_tensor_t* tensors, double* sum_squares, float* norm,
+ * infinite where the root is beyond float's range). */
+size_t ep_grad_norm_workspace_bytes(void);
+int ep_grad_norm(const ep_tensor_list_t* tensors, double* sum_squares, float* norm,
                  void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Every element times max_norm / norm, norm the root of *sum_squares, where norm
  * is larger than max_norm; as it is otherwise, and where norm is infinite or NaN
  * (the caller sees that from norm).
- *   into      NULL: in place.  Otherwise tensors of the same sizes, of either type
- *             each, that get the values; one may be the tensor itself, but
- *             otherwise none may overlap another
- *   max_norm  >= 0
- * The tensors must not overlap each other. */
-int ep_grad_clip(int32_t count, const ep_tensor_t* tensors, const ep_tensor_t* into,
+ *   into      NULL: in place.  Otherwise a list of as many tensors of the same
+ *             sizes, of either type each, that get the values; one may be the
+ *             tensor itself, but otherwise none may overlap any other of the two
+ *   max_norm  >= 0 */
+int ep_grad_clip(const ep_tensor_list_t* tensors, const ep_tensor_list_t* into,
                  const double* sum_squares, double max_norm, hipStream_t stream);
 
 /* ---- TransferCmd ring (UCCL-EP s2.2, s2.3, s5.2) ---------------------------

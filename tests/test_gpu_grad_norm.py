@@ -66,7 +66,8 @@ def check_clip(got, t, want_ratio):
 SIZES = {
     "one": [1], "seven": [7], "few": [5, 1, 0, 8, 9, 16385, 3], "unit": [16384, 16383, 16385, 32768],
     "edge": [8191, 8192, 8193, 16400], "many": [(i * 37) % 301 for i in range(1000)], "tables": [3] * 128 + [40000] + [5] * 200,
-    "large": [30_000_000, 11, 5_000_001], "empty": [0, 0, 0]}
+    "large": [30_000_000, 11, 5_000_001], "empty": [0, 0, 0],
+    "among empty": [0] * 70 + [40000] + [0] * 200 + [7, 16384 * 3] + [0] * 64 + [5]}
 
 
 @pytest.mark.parametrize("half", ["bf16", "float", "mixed"])
@@ -221,6 +222,7 @@ def test_a_list_holds_its_memory(ep):
 def test_refusals(ep):
     t = torch.ones(64, device="cuda")
     s, n, ws = torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda"), workspace(ep, 4)
+    assert len(ep.TensorList([t, t.clone()])) == 2
     for bad in ([t.half()], [t.double()], [t.cpu()], [t[::2]], [t, t], [t[:10], t[9:]], [t, t.cpu()], [t.view(8, 8).t()]):
         with pytest.raises(ValueError):
             ep.ep_grad_norm(bad, s, n, ws)

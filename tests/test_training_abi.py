@@ -120,46 +120,82 @@ def test_workspaces(ep):
     for bad in ((0, 8, 64, 64), (1, -1, 64, 64), (1, 8, 12, 64), (1, 8, 64, 4), (4097, 8, 64, 64), (1, 1 << 31, 64, 64)):
         assert need(*bad) == 0
     assert all(need(G, M, N, K) < 1 << 30 for G in (1, 7, 4096) for M in (0, 1, 10 ** 6, 2 ** 31 - 1) for N in (8, 4096) for K in (8, 4096))
-    assert ep.ep_grad_norm_workspace_bytes(0) > 0
-    assert ep.ep_grad_norm_workspace_bytes(1 << 20) < 1 << 26
-    assert ep.ep_grad_norm_workspace_bytes(-1) == 0
+    assert 0 < ep.ep_grad_norm_workspace_bytes() < 1 << 16
 
 
-def tensors(ep, *t):
-    return (ep.ep_tensor_t * max(1, len(t)))(*[ep.ep_tensor_t(*x) for x in t])
+def table(ep, *tensors, buffer=True, into=True):
+    """ep_tensor_table's status, the list and the bytes of the table."""
+    n = len(tensors)
+    a = (ep.ep_tensor_t * max(1, n))(*[ep.ep_tensor_t(*x) for x in tensors])
+    out, lst = ctypes.create_string_buffer(ep.lib.ep_tensor_table_bytes(n)), ep.ep_tensor_list_t()
+    st = ep.lib.ep_tensor_table(n, a, out if buffer else None, ctypes.byref(lst) if into else None)
+    return st, lst, out.raw
 
 
-def norm(ep, t, count=None, s=A, n=A, ws=A, bytes_=1 << 20):
-    return ep.lib.ep_grad_norm(len(t) if count is None else count, t, s, n, ws, bytes_, None)
-
-
-def clip(ep, t, into=None, count=None, s=A, bound=1.0):
-    return ep.lib.ep_grad_clip(len(t) if count is None else count, t, into, s, bound, None)
-
-
-BAD = [(A, -1, 0, 0), (A, 1 << 38, 0, 0), (A, 4, 2, 0), (A, 4, -1, 0), (None, 4, 0, 0), (A + 1, 4, 0, 0), (A + 2, 4, 1, 0)]
-
-
-@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("bad", [(A, -1, 0, 0), (A, 1 << 38, 0, 0), (A, 4, 2, 0), (A, 4, -1, 0), (None, 4, 0, 0), (A + 1, 4, 0, 0),
+                                 (A + 2, 4, 1, 0)])
 def test_a_bad_tensor(ep, bad):
-    good = (A, 8, 1, 0)
-    for t in (tensors(ep, bad), tensors(ep, good, bad)):
-        assert norm(ep, t) == INVALID
-        assert clip(ep, t) == INVALID
-    assert clip(ep, tensors(ep, (A, bad[1] if bad[1] > 0 else 4, 0, 0)), tensors(ep, bad)) == INVALID
+    assert table(ep, bad)[0] == INVALID
+    assert table(ep, (A, 8, 1, 0), bad)[0] == INVALID
+
+
+def test_table(ep):
+    assert ep.lib.ep_tensor_table_bytes(-1) == 0
+    assert table(ep, buffer=False)[0] == INVALID and table(ep, into=False)[0] == INVALID
+    st, lst, _ = table(ep)
+    assert st == 0 and lst.count == 0 and lst.units == 0
+    # a unit is 16384 elements from the first 128-byte boundary on; what lies before is the first's
+    sizes = [(A, 1, 1), (A + 4, 31, 1), (A + 4, 32, 1), (A, 0, 0), (A + 2, 16384 + 63, 0), (A + 2, 16384 + 64, 0), (None, 0, 1), (A, 1 << 30, 0)]
+    st, lst, raw = table(ep, *[(*x, 0) for x in sizes])
+    assert st == 0 and lst.count == 8
+    import struct
+    entries = [struct.unpack_from("<QqI", raw, 32 * i) for i in range(8)]
+    assert [e[2] for e in entries] == [0, 1, 2, 3, 3, 4, 6, 6]
+    assert struct.unpack_from("<I", raw, 32 * 8 + 16)[0] == lst.units == 6 + (1 << 16)
+    assert [e[0] for e in entries] == [(x[0] or 0) | x[2] for x in sizes] and [e[1] for e in entries] == [x[1] for x in sizes]
+    # too many units
+    assert table(ep, *[(A, (1 << 38) - 1, 0, 0)] * 129)[0] == INVALID
+    assert b"2^31" in ep.lib.ep_last_error()
+
+
+def listed(ep, *sizes, at=A):
+    lst = table(ep, *[(A, n, 0, 0) for n in sizes])[1]
+    lst.table = at
+    return lst
+
+
+def norm(ep, lst, s=A, n=A, ws=A, bytes_=1 << 20):
+    return ep.lib.ep_grad_norm(ctypes.byref(lst) if lst else None, s, n, ws, bytes_, None)
+
+
+def clip(ep, lst, into=None, s=A, bound=1.0):
+    return ep.lib.ep_grad_clip(ctypes.byref(lst) if lst else None, ctypes.byref(into) if into else None, s, bound, None)
+
+
+def test_lists_that_are_none(ep):
+    for lst in (None, listed(ep, 8, at=None), listed(ep, 8, at=A + 8)):
+        assert norm(ep, lst) == INVALID
+        assert clip(ep, lst) == INVALID
+        if lst is not None:
+            assert clip(ep, listed(ep, 8), lst) == INVALID
+    lst = listed(ep, 8)
+    lst.units = -1
+    assert norm(ep, lst) == INVALID and clip(ep, lst) == INVALID
+    lst.units = 1 << 31
+    assert norm(ep, lst) == INVALID
 
 
 def test_norm_refuses(ep):
-    t = tensors(ep, (A, 8, 0, 0))
-    for bad in (dict(count=-1), dict(s=None), dict(s=A + 4), dict(n=A + 2), dict(ws=None), dict(ws=A + 8), dict(bytes_=64)):
-        assert norm(ep, t, **bad) == INVALID, bad
-    assert ep.lib.ep_grad_norm(1, None, A, A, A, 1 << 20, None) == INVALID
+    lst = listed(ep, 8)
+    for bad in (dict(s=None), dict(s=A + 4), dict(n=A + 2), dict(ws=None), dict(ws=A + 8), dict(bytes_=64)):
+        assert norm(ep, lst, **bad) == INVALID, bad
 
 
 def test_clip_refuses(ep):
-    t = tensors(ep, (A, 8, 0, 0))
-    nan = float("nan")
-    for bad in (dict(count=-1), dict(s=None), dict(s=A + 4), dict(bound=-1.0), dict(bound=nan), dict(into=tensors(ep, (A, 9, 0, 0)))):
-        assert clip(ep, t, **bad) == INVALID, bad
-    assert clip(ep, tensors(ep), count=0) == 0
-    assert clip(ep, tensors(ep, (None, 0, 0, 0), (A, 0, 1, 0))) == 0
+    lst = listed(ep, 8, 9)
+    for bad in (dict(s=None), dict(s=A + 4), dict(bound=-1.0), dict(bound=float("nan")), dict(into=listed(ep, 8)),
+                dict(into=listed(ep, 9, 8)), dict(into=listed(ep, 8, 10))):
+        assert clip(ep, lst, **bad) == INVALID, bad
+    # nothing to launch
+    assert clip(ep, listed(ep, at=None)) == 0
+    assert clip(ep, listed(ep, 0, 0, at=None)) == 0
