@@ -61,6 +61,20 @@ __device__ inline float sigmoid(float g) {
     return far ? e : 1.0f / (1.0f + e);
 }
 
+// g * sigmoid(g), for the forward: through exp(-|g|), which never leaves float's range
+// upwards (nor, below -200, zero), by the hardware's exp2 and reciprocal (off by a unit in the last place each;
+// log2(e) in two parts, and scaled where the result is below float's normal range, which
+// that exp2 makes zero).  Half of sigmoid()'s instructions: a big tile's 128 results a lane,
+// with one wavefront on a SIMD, took 6 us with it.
+__device__ inline float silu(float g) {
+    const float x = fmaxf(-fabsf(g), -200.0f), t = x * 1.44269504f;
+    const float rest = fmaf(x, 1.44269504f, -t) + x * 1.92596300e-8f;
+    const bool low = t < -126.0f;
+    const float e = __builtin_amdgcn_exp2f(low ? t + 64.0f : t) * fmaf(rest, 0.693147181f, 1.0f) *
+                    (low ? 0x1p-64f : 1.0f);
+    return g * (g < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
 __device__ inline f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -97,23 +111,17 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
 
     for (int64_t id = blockIdx.x; id < a.tiles; id += gridDim.x) {
         // where the tile lies: P from p0 on, Q from q0 on (for the weights'
-        // gradient of expert e, else rows of e), c from block b0 to b1 of the
-        // `depth` values from c0 on
+        // gradient of expert e, else rows of e), c the `depth` values from c0 on
         const int p0 = (int)(id % a.tiles_w) * (MODE == kGate ? kSmall / 2 : kSmall);
         int64_t rest = id / a.tiles_w;
-        int e, b0, b1, q_count, part = 0;
+        int e, q_count;
         int64_t q0, c0 = 0, depth = a.C;
         if constexpr (MODE == kWeightBack) {
             q0 = (rest % a.tiles_v) * kSmall;
-            rest /= a.tiles_v;
-            part = (int)(rest % a.splits);
-            e = (int)(rest / a.splits);
+            e = (int)(rest / a.tiles_v);
             c0 = clamp_row(a.group_offset[e], a.M);
             depth = clamp_row(a.group_offset[e + 1], a.M) - c0;
             depth = depth < 0 ? 0 : depth;
-            const int64_t blocks = (depth + kDepth - 1) / kDepth;
-            b0 = (int)(blocks * part / a.splits);
-            b1 = (int)(blocks * (part + 1) / a.splits);
             q_count = a.V - (int)q0 < kSmall ? a.V - (int)q0 : kSmall;
         } else {
             const RowTile tile = find_tile(a.group_offset, a.G, a.M, rest, kSmall);
@@ -121,9 +129,8 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
             e = tile.g;
             q0 = tile.first;
             q_count = tile.count;
-            b0 = 0;
-            b1 = (a.C + kDepth - 1) / kDepth;
         }
+        const int blocks = (int)((depth + kDepth - 1) / kDepth);
 
         // Copies: lane's 16 bytes are chunk `lane % 8` of row 8 (2 wave + i) + lane / 8
         // of 128 bytes in LDS, i = 0, 1.  Along c: the row is an index of P (Q), and
@@ -153,7 +160,7 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
         if constexpr (!kQAcross)
             qbuf = buffer_rsrc(const_cast<uint16_t*>(a.q) + q0 * a.pitch_q, q_count * a.pitch_q * 2);
         const auto fetch = [&](int b, int stage) {
-            b = b < b1 ? b : b1 - 1;          // repeated behind the last block
+            b = b < blocks ? b : blocks - 1;  // repeated behind the last block
             uint8_t* l = s_mem + stage * kSmallBytes + wave * 2048;
             const int64_t left = depth - (int64_t)b * kDepth;
             const int rows = left < kDepth ? (int)left : kDepth, chunks = rows / 8;
@@ -191,14 +198,14 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
             for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const int at0 = r * 128 + (g ^ (r / 2)) * 16;
         const int f = r / 8 + g % 2 * 2, at_across = (8 * g + r / 4) * 128 + r % 4 * 8;
-        if (b0 < b1) {
+        if (blocks > 0) {
 #pragma unroll
             for (int s = 0; s < kSmallStages - 1; ++s) {
-                fetch(b0 + s, s);
+                fetch(s, s);
                 __builtin_amdgcn_sched_barrier(0);   // the meetings count on this order
             }
             int stage = 0;
-            for (int b = b0; b < b1; ++b) {
+            for (int b = 0; b < blocks; ++b) {
                 // block b is here when all but the two behind it are; everyone is then
                 // done with block b - 1, whose place the next copies take
                 meet<4 * (kSmallStages - 2), 0>();
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
                 const f32x4 gate = acc[0][j], up = acc[1][j];
                 float h[4];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) h[v] = gate[v] * sigmoid(gate[v]) * up[v];
+                for (int v = 0; v < 4; ++v) h[v] = silu(gate[v]) * up[v];
                 *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + qrow * F + c) =
                     u32x2{bf16_pack(h[0], h[1]), bf16_pack(h[2], h[3])};
                 if (a.pre) {
@@ -259,12 +266,11 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
                     const int c = p0 + wp * 32 + i * 16 + g * 4;
                     if (c >= a.W) continue;
                     const f32x4 v = acc[i][j];
+                    const int64_t at =
+                        (MODE == kWeightBack ? (int64_t)e * a.V + qrow : qrow) * a.W + c;
                     if (MODE == kWeightBack && a.wide) {
-                        const int64_t at = (((int64_t)part * a.G + e) * a.V + qrow) * a.W + c;
                         *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at) = v;
                     } else {
-                        const int64_t at =
-                            (MODE == kWeightBack ? (int64_t)e * a.V + qrow : qrow) * a.W + c;
                         *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
                             u32x2{bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3])};
                     }
@@ -304,7 +310,7 @@ __device__ inline int64_t uniform(int64_t v) {
 // round are 32 workgroups of one XCD, bands of 5 tiles along V.  (Up to 64 experts
 // are ordered, a lane each; with more, every workgroup has many.)
 struct WeightShare {
-    int64_t all, per_expert;
+    int64_t all, per_expert;      // per_expert: with its parts
     int32_t count, tiles_w, tiles_v, at;
     int32_t order;     // lane r: the expert with the r-th most rows
 
@@ -327,7 +333,7 @@ struct WeightShare {
         }
         tiles_w = a.tiles_w;
         tiles_v = a.tiles_v;
-        per_expert = (int64_t)tiles_w * tiles_v;
+        per_expert = (int64_t)tiles_w * tiles_v * a.splits;
         all = per_expert * a.G;
         at = (int)(blockIdx.x % 8u * (gridDim.x / 8u) + blockIdx.x / 8u);
         const int64_t rounds = all / gridDim.x;
@@ -336,9 +342,11 @@ struct WeightShare {
     __device__ int64_t index(int i) const {
         return (int64_t)i * gridDim.x + (i % 2 ? (int)gridDim.x - 1 - at : at);
     }
-    __device__ void place(const Bf16Args& a, int i, int* e, int* v, int* w) const {
+    __device__ void place(const Bf16Args& a, int i, int* e, int* part, int* v, int* w) const {
         const int64_t id = index(i), r = id / per_expert;
-        const int in = (int)(id - r * per_expert), wide = kBand * tiles_w, band = in / wide;
+        const int64_t one = (int64_t)tiles_w * tiles_v;
+        *part = (int)((id - r * per_expert) / one);
+        const int in = (int)((id - r * per_expert) % one), wide = kBand * tiles_w, band = in / wide;
         const int left = tiles_v - band * kBand, rows = left < kBand ? left : kBand;
         *e = a.G <= kWave ? bcast(order, (int)r) : (int)r;
         *v = band * kBand + (in - band * wide) % rows;
@@ -350,7 +358,7 @@ struct WeightShare {
 // first at c0.
 struct BigTile {
     int64_t q0, c0, depth;
-    int32_t e, p0, q_count, blocks;
+    int32_t e, part, p0, q_count, blocks;
 };
 
 template <int MODE, bool WIDE>
@@ -384,7 +392,7 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
         BigTile t;
         if constexpr (kWeights) {
             int v, w;
-            share.place(a, i, &t.e, &v, &w);
+            share.place(a, i, &t.e, &t.part, &v, &w);
             t.p0 = w * kBig;
             t.q0 = (int64_t)v * kBig;
             t.q_count = a.V - v * kBig < kBig ? a.V - v * kBig : kBig;
@@ -396,7 +404,15 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
                 t.depth = clamp_row(a.group_offset[t.e + 1], a.M) - t.c0;
                 if (t.depth < 0) t.depth = 0;
             }
+            if (a.splits > 1) {     // whole blocks
+                const int64_t blocks = (t.depth + kDepth - 1) / kDepth;
+                const int64_t b0 = blocks * t.part / a.splits, b1 = blocks * (t.part + 1) / a.splits;
+                const int64_t end = b1 * kDepth < t.depth ? b1 * kDepth : t.depth;
+                t.depth = b0 < b1 ? end - b0 * kDepth : 0;
+                t.c0 += b0 * kDepth;
+            }
         } else {
+            t.part = 0;
             int64_t m;
             int n;
             share.place(i, &m, &n);
@@ -415,6 +431,7 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
         t.c0 = uniform(t.c0);
         t.depth = uniform(t.depth);
         t.e = uniform(t.e);
+        t.part = uniform(t.part);
         t.p0 = uniform(t.p0);
         t.q_count = uniform(t.q_count);
         t.blocks = (int)((t.depth + kDepth - 1) / kDepth);
@@ -653,7 +670,8 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
                 const int c = i % (kBig / 8);
                 if (c >= vecs) continue;
                 const int64_t at =
-                    ((int64_t)t.e * a.V + t.q0 + i / (kBig / 8)) * a.W + t.p0 + c * 8;
+                    (((int64_t)t.part * a.G + t.e) * a.V + t.q0 + i / (kBig / 8)) * a.W + t.p0 +
+                    c * 8;
                 u32x4* out = reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(a.out) +
                                                       at * (WIDE ? 4 : 2));
                 out[0] = u32x4{0, 0, 0, 0};
@@ -704,14 +722,13 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                const float gate = acc[i + k][j][v];
-                                h[k][v] = gate * sigmoid(gate) * acc[i + k + 4][j][v];
-                            }
+                            for (int v = 0; v < 4; ++v)
+                                h[k][v] = silu(acc[i + k][j][v]) * acc[i + k + 4][j][v];
                         store8(h[0], h[1], reinterpret_cast<uint16_t*>(a.out) + qrow * F, first, F);
                     }
                 } else {
-                    const int64_t at = (kWeights ? (int64_t)t.e * a.V + qrow : qrow) * a.W;
+                    const int64_t at =
+                        (kWeights ? ((int64_t)t.part * a.G + t.e) * a.V + qrow : qrow) * a.W;
                     const int first = t.p0 + wp * 128;
                     if constexpr (WIDE) {
                         float* out = reinterpret_cast<float*>(a.out) + at;
@@ -808,13 +825,13 @@ int check_bf16(int32_t G, int64_t M, int32_t N, int32_t K) {
     return EP_OK;
 }
 
-// Parts of c that a weights' gradient is cut into: as many as give two rounds of
-// the CUs, but at least four blocks of the average expert's rows each.
+// Parts of c that a weights' gradient is cut into: as many as give every CU a big tile,
+// but at least eight blocks of the average expert's rows each.
 int32_t weight_splits(int32_t G, int64_t M, int32_t N, int32_t K) {
-    const int64_t tiles = (int64_t)G * ceil_div(N, kSmall) * ceil_div(K, kSmall);
-    const int64_t most = ceil_div(ceil_div(M, G), 4 * kDepth);
-    const int64_t want = ceil_div(1024, tiles);
-    return (int32_t)(want < most ? want : (most < 1 ? 1 : most));
+    const int64_t tiles = (int64_t)G * ceil_div(N, kBig) * ceil_div(K, kBig);
+    const int64_t most = ceil_div(ceil_div(M, G), 8 * kDepth);
+    const int64_t want = kBigGrid / tiles;
+    return (int32_t)(want < most ? (want < 1 ? 1 : want) : (most < 1 ? 1 : most));
 }
 
 }  // namespace ep
@@ -841,7 +858,7 @@ int launch_small(Bf16Args& a, hipStream_t stream) {
     a.tiles_w = (int32_t)(MODE == kGate ? ceil_div(a.W / 2, kSmall / 2) : ceil_div(a.W, kSmall));
     if (MODE == kWeightBack) {
         a.tiles_v = (int32_t)ceil_div(a.V, kSmall);
-        a.tiles = (int64_t)a.G * a.splits * a.tiles_v * a.tiles_w;
+        a.tiles = (int64_t)a.G * a.tiles_v * a.tiles_w;
     } else {
         a.tiles = max_tiles(a.M, a.G, kSmall) * a.tiles_w;
     }
@@ -859,7 +876,7 @@ int launch_big(Bf16Args& a, hipStream_t stream) {
     a.tiles_w = (int32_t)(MODE == kGate ? ceil_div(a.W / 2, kBig / 2) : ceil_div(a.W, kBig));
     if (MODE == kWeightBack) {
         a.tiles_v = (int32_t)ceil_div(a.V, kBig);
-        a.tiles = (int64_t)a.G * a.tiles_v * a.tiles_w;
+        a.tiles = (int64_t)a.G * a.splits * a.tiles_v * a.tiles_w;
     } else {
         a.tiles = max_tiles(a.M, a.G, kBig) * a.tiles_w;
     }
@@ -875,12 +892,52 @@ int launch_big(Bf16Args& a, hipStream_t stream) {
     return EP_OK;
 }
 
+// Which tiles take less time, from what each kind costs (ns):
+//   small  the weights once from memory (5.4 TB/s) or once for every 64 rows from cache
+//          (7.5 TB/s), a third more where their rows do not begin on lines; 4 us
+//   big    rounds of tiles over the CUs, 1.25 us a block of c; 10 us, for the gate 20; no
+//          less than the weights at 4.4 TB/s
+// Small : big, us, as measured (rows an expert; e: even, s: falling off as 1 / rank):
+//   forward, 8 experts of 7168 x 1792   1  39 : 47   32 e  43 : 46   64 e 50 : 46   256 e 118 : 55
+//   forward, 8 of 3584 x 7168          64 e  91 : 139  128 e 144 : 143  192 s 198 : 146
+//   forward, 24 of 1808 x 2184         16 e  53 : 63    64 s  76 : 72   256 e 169 : 78
+//   forward, 1 of 7168 x 1792         512  29 : 44    32 of 512 x 1024  128 e 18 : 27  512 s 50 : 32
+//   rows, 8 of 7168 x 1792             64 e  49 : 133  256 e 138 : 156  512 s 247 : 156
+//   rows, 8 of 3584 x 7168              1  83 : 79   128 e 155 : 86
+template <int MODE>
+bool big_takes_less(const Bf16Args& a) {
+    const int64_t experts = a.G < a.M ? a.G : a.M;      // that can have rows
+    const int64_t weights = (int64_t)a.W * a.C * 2;
+    const int64_t small_rows = a.M / kSmall + (experts + 1) / 2;
+    int64_t small = experts * weights / 5400;
+    if (small_rows * weights / 7500 > small) small = small_rows * weights / 7500;
+    if (a.pitch_p % kDepth != 0) small += small / 3;
+    small += 4000;
+    const int64_t most_rows = a.M / kBig + (experts + 1) / 2;
+    const int64_t tiles = (most_rows > experts ? most_rows : experts) *
+                          (MODE == kGate ? ceil_div(a.W / 2, kBig / 2) : ceil_div(a.W, kBig));
+    int64_t big = ceil_div(tiles, kBigGrid) * ceil_div(a.C, kDepth) * 1250 + (MODE == kGate ? 20000 : 10000);
+    if (experts * weights / 4400 + 5000 > big) big = experts * weights / 4400 + 5000;
+    return big <= small;
+}
+
 template <int MODE>
 int launch(Bf16Args& a, hipStream_t stream) {
-    if (a.M >= (int64_t)a.G * 128 && a.splits == 1)
-        return a.wide ? launch_big<MODE, MODE == kWeightBack>(a, stream)
-                      : launch_big<MODE, false>(a, stream);
-    return launch_small<MODE>(a, stream);
+    return big_takes_less<MODE>(a) ? launch_big<MODE, false>(a, stream) : launch_small<MODE>(a, stream);
+}
+
+// The weights' gradient: big tiles write it faster (8 rows of 8 experts, 7168 x 1792:
+// 52 : 145 us) and, in parts, take a long sum apart.  Only where an expert's few tiles may
+// have many of the rows, no tile can be dealt against them: small ones there (32 experts of
+// 512 x 1024, 256 rows each, falling off as 1 / rank 37 : 50 us, even 36 : 20; 512 each 51 :
+// 87 and 50 : 26).
+template <>
+int launch<kWeightBack>(Bf16Args& a, hipStream_t stream) {
+    const int64_t tiles = (int64_t)a.G * a.splits * ceil_div(a.V, kBig) * ceil_div(a.W, kBig);
+    if (a.G > 1 && a.splits == 1 && tiles < 2 * kBigGrid && a.M >= 32 * kBig)
+        return launch_small<kWeightBack>(a, stream);
+    return a.wide ? launch_big<kWeightBack, true>(a, stream)
+                  : launch_big<kWeightBack, false>(a, stream);
 }
 
 int forward(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,

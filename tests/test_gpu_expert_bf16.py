@@ -206,6 +206,42 @@ def test_many_rows(ep, sizes, N, K):
     assert int(c.st) == 0
 
 
+def test_gates_far_from_zero(ep):
+    """One row, one weight: the gates are what they are said to be."""
+    g = [-3e38, -1e4, -205.0, -199.0, -103.5, -95.0, -89.0, -88.5, -87.0, -80.5, -79.5, -20.0, -1.0, -1e-30, 0.0, 1e-30, 1.0, 20.0, 88.0, 3e38,
+         float("inf"), float("-inf"), float("nan"), 0.5]
+    F, K = len(g), 8
+    w = torch.zeros(1, 2 * F, K, **BF)
+    w[0, :F, 0] = torch.tensor(g)
+    w[0, F:, 0] = 3.0
+    rows = torch.zeros(1, K, **BF)
+    rows[0, 0] = 1.0
+    off, st = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.zeros(1, F, **BF)
+    for copies in (1, 300):        # small and big tiles
+        x = rows.repeat(copies, 1)
+        out = torch.zeros(copies, F, **BF)
+        off[1] = copies
+        ep.ep_expert_gate_up_bf16(x, off, w, None, out, st)
+        gate = w[0, :F, 0].double()
+        want = torch.where(gate == float("-inf"), float("nan"), gate * torch.sigmoid(gate) * 3.0).expand(copies, F)
+        want = torch.where(want.abs() > 3.4e38, want.bfloat16().double(), want)      # beyond bf16: infinite
+        tol = X.bf16_tol(want, 8 * 4 * X.U32 * want.abs() + (gate * 3.0).abs() * 2.0 ** -149)
+        assert_close(out, want, torch.nan_to_num(tol, 0.0, 0.0, 0.0), "gated")
+
+
+def test_a_long_sum_in_parts(ep):
+    """Few weights, many rows: the weights' gradient is summed in parts."""
+    for sizes, N, K in (([30000], 64, 72), ([5000, 0, 9000], 264, 520), ([700], 8, 8)):
+        c = Case(sizes, N, K, 1, 2, whole=True, seed=12)
+        assert sum(sizes) < 1000 or ep.ep_expert_backward_workspace_bytes(c.G, c.M, N, K) > 0
+        for kind in (torch.bfloat16, torch.float32):
+            gw = torch.full((c.G, N, K), POISON, dtype=kind, device="cuda")
+            ep.ep_expert_product_bf16_backward(c.rows, c.off, None, c.grad_out, None, gw, c.st, c.workspace(ep))
+            c.close(gw, *X.weights64(c.rows, c.off, c.grad_out), max(sizes), "grad_w")
+        assert int(c.st) == 0
+
+
 def test_differences(ep):
     """Central differences of the library's own forward in a direction, against its
     gradients: whole numbers make the plain product exact."""
