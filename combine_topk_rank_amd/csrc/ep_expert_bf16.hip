@@ -94,7 +94,9 @@ __device__ inline __attribute__((always_inline)) bf16x8 lds_across(const uint8_t
 
 // ---- Small tiles ------------------------------------------------------------------
 // 64 x 64 outputs a workgroup of four wavefronts, 32 x 32 each; four blocks of c
-// of both operands in LDS, 16 KB each, three under way.
+// of both operands in LDS, 16 KB each, three under way.  For few rows: bound by the
+// weights' way from memory (one row at each of 8 experts, 7168 x 1792, 206 MB: 39 us,
+// 5.3 TB/s).
 constexpr int kSmall = 64;
 constexpr int kSmallStages = 4;
 constexpr int kSmallBytes = 2 * kSmall * 128;
@@ -281,16 +283,25 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
 }
 
 // ---- Big tiles --------------------------------------------------------------------
-// 256 x 256 outputs a workgroup of eight wavefronts, one workgroup a CU, which
-// works through its share of tiles.  The blocks of c of both operands, 32 KB each,
-// go from memory to LDS ahead of their use, two blocks ahead and on into the next
-// tile: three blocks of P and two of Q fill the 160 KB.  A wavefront has 128 of P
-// x 64 of Q.
+// 256 x 256 outputs a workgroup of four wavefronts, one workgroup a CU, which works
+// through its share of tiles.  The blocks of c of both operands, 32 KB each, go from
+// memory to LDS ahead of their use, two blocks ahead and on into the next tile: three
+// blocks of P and two of Q fill the 160 KB.  A wavefront, one on a SIMD, has 128 x 128
+// results in all 256 accumulation registers: eight wavefronts of 128 x 64 read half as
+// much again from LDS and took 5 % longer.
+//
+// Bound by the card's power: with random numbers in the operands a block takes 1.38 us
+// (clock lowered to about 1.6 GHz), with zeros 1.06; a bare loop of these MFMAs (16 x 16 x
+// 32; 32 x 32 x 16 draw more) reaches 2.0 PFLOP/s with random numbers.  8192 x 8192 x
+// 7168, the card warm: forward 1.46 PFLOP/s, rows' gradient 1.33, weights' 1.33; the
+// library's product of the same operands 1.6, 1.2, 0.9.  About 8 us a tile go to its
+// beginning and end, 4 of them to stores, which all CUs have at once: 7680 rows of 8
+// experts, 7168 x 1792, 183 us (1.08 PFLOP/s; 34 row tiles for 30 tiles' rows, and 3.7
+// rounds of the CUs run as four).
 constexpr int kBig = 256;
-constexpr int kBigWaves = 4;
-constexpr int kBigThreads = kBigWaves * kWave;
-constexpr int kBigCopies = 32 / kBigWaves;      // a wavefront's copies of a block of an operand
-constexpr int kBigQTiles = 32 / kBigWaves;      // its tiles of 16 along Q
+constexpr int kBigThreads = 256;
+constexpr int kBigCopies = 8;                   // a wavefront's copies of a block of an operand
+constexpr int kBigTiles = 8;                    // its tiles of 16 along P, and along Q
 constexpr int kBigGrid = 256;                   // CUs of the GPU: one workgroup fills a CU's LDS
 constexpr int kOperandBytes = kBig * kDepth * 2;
 constexpr int kQAt = 3 * kOperandBytes;         // LDS: three blocks of P, two of Q
@@ -362,14 +373,15 @@ struct BigTile {
 };
 
 template <int MODE, bool WIDE>
-__global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void bf16_big_kernel(Bf16Args a) {
+__global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void bf16_big_kernel(Bf16Args a) {
     constexpr bool kPAcross = MODE == kRowsBack || MODE == kWeightBack;
     constexpr bool kQAcross = MODE == kWeightBack;
     constexpr bool kGateUp = MODE == kGate, kWeights = MODE == kWeightBack;
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[5 * kOperandBytes];
     if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-    const int wp = wave % 2, wq = wave / 2;     // neighbours share Q: those without any idle alike
+    const int wp = wave % 2, wq = wave / 2;
     const auto share = [&]() {
         if constexpr (kWeights) {
             return WeightShare(a);
@@ -439,9 +451,9 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
     };
 
     // Where the copies stand: block `fb` of tile `ft`.  Along c a wavefront copies
-    // rows wave * 32 + 8 i + lane / 8 of an operand, chunk c of row q to chunk
+    // rows 64 wave + 8 i + lane / 8 of an operand, chunk c of row q to chunk
     // c ^ (q / 2 % 8) of its 128 bytes.  Across, c's of a block are rows of 512 bytes,
-    // two an instruction, wave * 8 + 2 i + lane / 32; the 32 bytes of row c which a
+    // two an instruction, 16 wave + 2 i + lane / 32; the 32 bytes of row c which a
     // tile of 16 columns takes sit at ^ f, f = c % 4 + 4 (c / 8 % 2), so that the
     // eight rows which half a wavefront reads meet all banks once.  The buffers' ends
     // and what lies behind them are as in the small tiles.
@@ -501,11 +513,11 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
         if constexpr (kPAcross)
             op[i] = (uint32_t)(wave * 2 * kBigCopies + lane / 32) * pitch_p +
                     ((lane % 32) ^ (lane / 32 * 2) ^ (i % 2 * 4) ^
-                     ((wave * kBigCopies / 4 + i / 2) % 2 * 8)) * 16;
+                     (i / 2 * 8)) * 16;
         if constexpr (kQAcross)
             oq[i] = (uint32_t)(wave * 2 * kBigCopies + lane / 32) * pitch_q +
                     ((lane % 32) ^ (lane / 32 * 2) ^ (i % 2 * 4) ^
-                     ((wave * kBigCopies / 4 + i / 2) % 2 * 8)) * 16;
+                     (i / 2 * 8)) * 16;
     }
     // behind the last tile the copies repeat its last block
     const auto advance = [&]() {
@@ -553,7 +565,7 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
     const int r = lane % 16, g = lane / 16;
     const int along = r * 128 + (g ^ (r / 2)) * 16;
     const int fold = r / 4 + g % 2 * 4, across = (8 * g + r / 4) * 512 + r % 4 * 8;
-    const int across_p = across + ((wp * 8) ^ fold) * 32, across_q = across + ((wq * kBigQTiles) ^ fold) * 32;
+    const int across_p = across + ((wp * 8) ^ fold) * 32, across_q = across + ((wq * kBigTiles) ^ fold) * 32;
     const auto ptile = [&](uint32_t at, int i, int h) {
         if constexpr (kPAcross)
             return lds_across(s_mem + at + (across_p ^ (i * 32)) + h * 16384, 2048);
@@ -564,7 +576,7 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
         if constexpr (kQAcross)
             return lds_across(s_mem + at + (across_q ^ (j * 32)) + h * 16384, 2048);
         else
-            return lds16(s_mem + at + (wq * kBigQTiles + j) * 2048 + (along ^ (h * 64)));
+            return lds16(s_mem + at + (wq * kBigTiles + j) * 2048 + (along ^ (h * 64)));
     };
 
     // the first tile with a block
@@ -577,8 +589,8 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
     // places of this, the next and the over-next block
     uint32_t p_at[3] = {0, kOperandBytes, 2 * kOperandBytes};
     uint32_t q_at[2] = {kQAt, kQAt + kOperandBytes};
-    f32x4 acc[8][kBigQTiles];
-    bf16x8 p[4][2], q[2][kBigQTiles];
+    f32x4 acc[8][kBigTiles];
+    bf16x8 p[4][2], q[2][kBigTiles];
     if (any) {
         aim();
 #pragma unroll
@@ -597,7 +609,7 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < kBigQTiles; ++j) q[h][j] = qtile(q_at[0], j, h);
+            for (int j = 0; j < kBigTiles; ++j) q[h][j] = qtile(q_at[0], j, h);
             p[0][h] = ptile(p_at[0], 0, h);
             p[1][h] = ptile(p_at[0], 1, h);
         }
@@ -689,8 +701,8 @@ __global__ __launch_bounds__(kBigThreads) __attribute__((amdgpu_waves_per_eu(1, 
             int row = lane % 16, group = lane / 16;
             asm volatile("" : "+v"(row), "+v"(group));
 #pragma unroll
-            for (int j = 0; j < kBigQTiles; ++j) {
-                const int qi = (wq * kBigQTiles + j) * 16 + row;
+            for (int j = 0; j < kBigTiles; ++j) {
+                const int qi = (wq * kBigTiles + j) * 16 + row;
                 const int64_t qrow = t.q0 + qi;
                 const bool in = qi < t.q_count;
                 // A lane has columns 4 group .. 4 group + 3 of each 16: two neighbouring
@@ -776,7 +788,7 @@ __global__ __launch_bounds__(256) void weight_join_kernel(JoinArgs a) {
 
 // ---- The gate's backward ------------------------------------------------------------
 // grad_gate = d * u * s * (1 + g * (1 - s)), grad_up = d * g * s, s = sigmoid(g).
-// A thread has eight outputs of a row at a time, 2^tpr_log threads a row.
+// A thread has eight outputs of a row at a time, 2^tpr_log threads a row.  Bound by memory.
 // d's products come first: of two bf16 values they are exact in float.  Each
 // operation is rounded by itself (no fused multiply-add), as elementary float
 // operations are.
@@ -906,19 +918,16 @@ int launch_big(Bf16Args& a, hipStream_t stream) {
 //   rows, 8 of 3584 x 7168              1  83 : 79   128 e 155 : 86
 template <int MODE>
 bool big_takes_less(const Bf16Args& a) {
-    const int64_t experts = a.G < a.M ? a.G : a.M;      // that can have rows
-    const int64_t weights = (int64_t)a.W * a.C * 2;
-    const int64_t small_rows = a.M / kSmall + (experts + 1) / 2;
-    int64_t small = experts * weights / 5400;
-    if (small_rows * weights / 7500 > small) small = small_rows * weights / 7500;
-    if (a.pitch_p % kDepth != 0) small += small / 3;
-    small += 4000;
-    const int64_t most_rows = a.M / kBig + (experts + 1) / 2;
-    const int64_t tiles = (most_rows > experts ? most_rows : experts) *
-                          (MODE == kGate ? ceil_div(a.W / 2, kBig / 2) : ceil_div(a.W, kBig));
-    int64_t big = ceil_div(tiles, kBigGrid) * ceil_div(a.C, kDepth) * 1250 + (MODE == kGate ? 20000 : 10000);
-    if (experts * weights / 4400 + 5000 > big) big = experts * weights / 4400 + 5000;
-    return big <= small;
+    const double experts = a.G < a.M ? a.G : (double)a.M;     // that can have rows
+    const double weights = 2.0 * a.W * a.C;
+    const double per64 = (double)(a.M / kSmall) + 0.5 * experts;
+    double small = fmax(experts * weights / 5400.0, per64 * weights / 7500.0);
+    if (a.pitch_p % kDepth != 0) small *= 4.0 / 3.0;
+    const double row_tiles = fmax(experts, (double)(a.M / kBig) + 0.5 * experts);
+    const double columns = MODE == kGate ? ceil_div(a.W / 2, kBig / 2) : ceil_div(a.W, kBig);
+    const double rounds = ceil(row_tiles * columns / kBigGrid);
+    const double big = rounds * ceil_div(a.C, kDepth) * 1250.0 + (MODE == kGate ? 20000.0 : 10000.0);
+    return fmax(big, experts * weights / 4400.0 + 5000.0) <= small + 4000.0;
 }
 
 template <int MODE>

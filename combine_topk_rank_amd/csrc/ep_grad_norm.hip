@@ -12,6 +12,10 @@
 //
 // The clip: v * m * 2^e with max_norm / norm = m * 2^e, so a ratio below float's
 // range still scales what float holds.
+//
+// Bound by memory.  40 tensors of 622 MB, nearly all bf16: norm 111 us (5.6 TB/s), clip
+// into other buffers 241 us (5.2), both in a row 330: the clip finds the last 200 MB in the
+// last-level cache.  1000 tensors of 156 MB: norm 33 us.
 
 #include <string.h>
 
@@ -24,7 +28,8 @@ constexpr int kGradGrid = 512;            // two workgroups a CU
 constexpr int kUnitVecs = 2;              // groups of 8 elements a thread
 constexpr int kUnit = kGradThreads * 8 * kUnitVecs;
 constexpr int kHeld = 1024;               // tensors whose entries a workgroup holds in LDS
-constexpr int kMostChunk = 2;             // units that a workgroup takes at a time
+constexpr int kMostChunk = 2;             // units that a workgroup takes at a time: with 1 the
+                                          // 622 MB's norm and clip take 377 us, 2 340, 4 352, 8 369
 constexpr int64_t kMaxTensor = (int64_t)1 << 38;   // elements
 constexpr int64_t kMaxUnits = (int64_t)1 << 31;
 
@@ -85,6 +90,7 @@ __device__ inline void walk(const GradArgs& a, EIGHT eight, ONE one) {
     __shared__ uint32_t s_first[kHeld + 1];
     __shared__ uint64_t s_from[kHeld], s_to[CLIP ? kHeld : 1];
     __shared__ int64_t s_n[kHeld];
+    if (a.units == 0) return;      // there may be no table
     const bool held = a.count <= kHeld;
     const int tid = (int)threadIdx.x;
     for (int i = tid; held && i <= a.count; i += kGradThreads) {

@@ -67,7 +67,7 @@ SIZES = {
     "one": [1], "seven": [7], "few": [5, 1, 0, 8, 9, 16385, 3], "unit": [16384, 16383, 16385, 32768],
     "edge": [8191, 8192, 8193, 16400], "many": [(i * 37) % 301 for i in range(1000)], "tables": [3] * 128 + [40000] + [5] * 200,
     "large": [30_000_000, 11, 5_000_001], "empty": [0, 0, 0],
-    "among empty": [0] * 70 + [40000] + [0] * 200 + [7, 16384 * 3] + [0] * 64 + [5]}
+    "thousands": [(i * 61) % 977 for i in range(3000)], "among empty": [0] * 70 + [40000] + [0] * 200 + [7, 16384 * 3] + [0] * 64 + [5]}
 
 
 @pytest.mark.parametrize("half", ["bf16", "float", "mixed"])
@@ -217,6 +217,19 @@ def test_a_list_holds_its_memory(ep):
     s2, _ = torch.zeros(1, dtype=torch.float64, device="cuda"), None
     ep.ep_grad_norm(tl, s2, None, workspace(ep, 1))
     assert float(s) == 1000.0 and float(s2) == 1000.0
+
+
+def test_lists_without_elements(ep):
+    """No table is followed where there is nothing: the C call takes NULL then."""
+    import ctypes
+    s, ws = torch.full((1,), -1.0, dtype=torch.float64, device="cuda"), workspace(ep, 0)
+    for tensors in ([], [torch.empty(0, device="cuda")] * 3):
+        tl = ep.TensorList(tensors)
+        tl.c.table = None
+        assert ep.lib.ep_grad_norm(ctypes.byref(tl.c), s.data_ptr(), None, ws.data_ptr(), ws.numel(), None) == 0
+        torch.cuda.synchronize()
+        assert float(s) == 0.0
+        s.fill_(-1.0)
 
 
 def test_refusals(ep):
