@@ -41,6 +41,7 @@ struct Bf16Args {
     int32_t* st;
     int64_t M;
     int64_t tiles;                 // of the launch
+    int64_t places;                // small tiles: with what fills the runs up
     int32_t G;
     int32_t W;                     // P's extent outside c (gate: 2F)
     int32_t V;                     // weights' gradient: Q's extent outside c
@@ -97,21 +98,41 @@ __device__ inline __attribute__((always_inline)) bf16x8 lds_across(const uint8_t
 // of both operands in LDS, 16 KB each, three under way.  For few rows: bound by the
 // weights' way from memory (one row at each of 8 experts, 7168 x 1792, 206 MB: 39 us,
 // 5.3 TB/s).
+//
+// Rows along c that do not begin on 128-byte lines are copied by lines all the same: a
+// row's chunk comes with block b's copies where it lies in the same line as the block's
+// first chunk, else with block b + 1's, and is read from there.  That takes a fifth block
+// in LDS.  Copies of 128 bytes across two lines would ask for both, for each of them
+// twice (24 experts of 1808 x 2184, 1436 rows falling off as 1 / rank: forward 56 us, by
+// blocks 71; of 1808 x 2208, on half lines, 56 : 62).  Where all rows begin on lines,
+// four blocks with nothing to look up: 39 us for the one row an expert above, against 40.
 constexpr int kSmall = 64;
-constexpr int kSmallStages = 4;
 constexpr int kSmallBytes = 2 * kSmall * 128;
 constexpr int kSmallThreads = 256;
+// Across, the tiles beside each other share lines at their border where rows do not
+// begin on lines.  Workgroups go to the eight XCDs in turn: each gets runs of this many
+// tiles, so that such a line comes to its L2 once (rows' gradient, 8 experts of 7168 x
+// 1800, one row each: 59 us one by one, 44 in eights; 16384 rows of 32 experts of 512 x
+// 1032, weights' gradient: 66 and 57; where rows begin on lines mostly within 3 %, 4 experts
+// of 5120 x 5120, 300 rows falling off, 86 and 78).
+constexpr int kRun = 8;
 
-template <int MODE>
+template <int MODE, bool LINES>
 __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a) {
     constexpr bool kPAcross = MODE == kRowsBack || MODE == kWeightBack;
     constexpr bool kQAcross = MODE == kWeightBack;
-    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[kSmallStages * kSmallBytes];
+    constexpr int kStages = LINES ? 4 : 5, kNeeded = LINES ? 1 : 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[kStages * kSmallBytes];
     if (blockIdx.x == 0) check_groups(a.group_offset, a.G, a.M, a.st);
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int wp = wave % 2, wq = wave / 2, r = lane % 16, g = lane / 16;
 
-    for (int64_t id = blockIdx.x; id < a.tiles; id += gridDim.x) {
+    for (int64_t place = blockIdx.x; place < a.places; place += gridDim.x) {
+        int64_t id = place;
+        if constexpr (kPAcross) {
+            id = (place / (8 * kRun) * 8 + place % 8) * kRun + place / 8 % kRun;
+            if (id >= a.tiles) continue;
+        }
         // where the tile lies: P from p0 on, Q from q0 on (for the weights'
         // gradient of expert e, else rows of e), c the `depth` values from c0 on
         const int p0 = (int)(id % a.tiles_w) * (MODE == kGate ? kSmall / 2 : kSmall);
@@ -147,6 +168,12 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
         const int prow = MODE == kGate ? lane / 8 : row;
         const int along = (lane % 8) ^ (lane / 16), across = (lane % 8) ^ (lane / 16 % 2 * 2);
         __amdgpu_buffer_rsrc_t pbuf, qbuf;
+        // Chunks of 16 bytes from the beginning of a line to that of a row along c
+        const auto behind_line = [](const uint16_t* x, int64_t row, int pitch) {
+            return LINES ? 0 : (int)(((uintptr_t)(x + row * pitch) >> 4) & 7);
+        };
+        int p_from[2] = {0, 0}, q_from[2] = {0, 0};   // the copied row's chunk, in block 0
+        const auto from = [](int c, int behind) { return c + behind < 8 ? c : c - 8; };
         if constexpr (!kPAcross) {
             int first = p0, extent = a.W, most = kSmall;
             if constexpr (MODE == kGate) {    // a wavefront copies 16 gates or 16 ups
@@ -158,14 +185,23 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
             const int rows = extent - first < most ? extent - first : most;
             pbuf = buffer_rsrc(const_cast<uint16_t*>(a.p) + ((int64_t)e * a.W + first) * a.pitch_p,
                                rows * a.pitch_p * 2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                p_from[i] = from(along ^ (4 * i),
+                                 behind_line(a.p, (int64_t)e * a.W + first + prow + 8 * i, a.pitch_p));
         }
-        if constexpr (!kQAcross)
+        if constexpr (!kQAcross) {
             qbuf = buffer_rsrc(const_cast<uint16_t*>(a.q) + q0 * a.pitch_q, q_count * a.pitch_q * 2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                q_from[i] = from(along ^ (4 * i), behind_line(a.q, q0 + row + 8 * i, a.pitch_q));
+        }
         const auto fetch = [&](int b, int stage) {
-            b = b < blocks ? b : blocks - 1;  // repeated behind the last block
             uint8_t* l = s_mem + stage * kSmallBytes + wave * 2048;
+            const int chunk = b * 8, chunks = (int)(depth / 8);   // depth: a multiple of 8, or across
+            b = b < blocks ? b : blocks - 1;  // across: repeated behind the last block
             const int64_t left = depth - (int64_t)b * kDepth;
-            const int rows = left < kDepth ? (int)left : kDepth, chunks = rows / 8;
+            const int rows = left < kDepth ? (int)left : kDepth;
             if constexpr (kPAcross) {
                 const int64_t from = MODE == kRowsBack ? (int64_t)e * a.C : c0;
                 pbuf = buffer_rsrc(const_cast<uint16_t*>(a.p) +
@@ -178,17 +214,18 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
                                    (rows * a.pitch_q - (int)q0) * 2);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int c = along ^ (4 * i);
                 uint32_t at = (uint32_t)((prow + 8 * i) * a.pitch_p * 2);
                 if constexpr (kPAcross)
                     to_lds(pbuf, at + (across ^ (4 * i)) * 16, 0, l + i * 1024);
                 else
-                    to_lds(pbuf, c < chunks ? at + c * 16 : 0x80000000u, b * 128, l + i * 1024);
+                    to_lds(pbuf, (uint32_t)(chunk + p_from[i]) < (uint32_t)chunks
+                                     ? at + (chunk + p_from[i]) * 16 : 0x80000000u, 0, l + i * 1024);
                 at = (uint32_t)((row + 8 * i) * a.pitch_q * 2);
                 if constexpr (kQAcross)
                     to_lds(qbuf, at + (across ^ (4 * i)) * 16, 0, l + kSmall * 128 + i * 1024);
                 else
-                    to_lds(qbuf, c < chunks ? at + c * 16 : 0x80000000u, b * 128,
+                    to_lds(qbuf, (uint32_t)(chunk + q_from[i]) < (uint32_t)chunks
+                                     ? at + (chunk + q_from[i]) * 16 : 0x80000000u, 0,
                            l + kSmall * 128 + i * 1024);
             }
         };
@@ -200,21 +237,33 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
             for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const int at0 = r * 128 + (g ^ (r / 2)) * 16;
         const int f = r / 8 + g % 2 * 2, at_across = (8 * g + r / 4) * 128 + r % 4 * 8;
+        // how far behind its line's beginning each row of the lane's tiles begins
+        int p_behind[2], q_behind[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int tp = wp * 2 + i, tq = wq * 2 + i;
+            const int64_t prow0 = MODE == kGate ? p0 + tp / 2 * 16 + tp % 2 * (a.W / 2) : p0 + tp * 16;
+            p_behind[i] = behind_line(a.p, (int64_t)e * a.W + prow0 + r, a.pitch_p);
+            q_behind[i] = behind_line(a.q, q0 + tq * 16 + r, a.pitch_q);
+        }
         if (blocks > 0) {
 #pragma unroll
-            for (int s = 0; s < kSmallStages - 1; ++s) {
+            for (int s = 0; s < kStages - 1; ++s) {
                 fetch(s, s);
                 __builtin_amdgcn_sched_barrier(0);   // the meetings count on this order
             }
             int stage = 0;
             for (int b = 0; b < blocks; ++b) {
-                // block b is here when all but the two behind it are; everyone is then
-                // done with block b - 1, whose place the next copies take
-                meet<4 * (kSmallStages - 2), 0>();
-                fetch(b + kSmallStages - 1, (stage + kSmallStages - 1) % kSmallStages);
+                // block b, and the next copies, which may hold the last of it, are here
+                // when all but the two behind are; everyone is then done with block
+                // b - 1, whose place the next copies take
+                meet<4 * (kStages - 1 - kNeeded), 0>();
+                fetch(b + kStages - 1, (stage + kStages - 1) % kStages);
                 __builtin_amdgcn_sched_barrier(0);
+                const int next = (stage + 1) % kStages;
                 const uint8_t* lp = s_mem + stage * kSmallBytes;
                 const uint8_t* lq = lp + kSmall * 128;
+                const int later = (next - stage) * kSmallBytes;
                 bf16x8 p[2][2], q[2][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -224,11 +273,13 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
                         if constexpr (kPAcross)
                             p[h][i] = lds_across(lp + h * 4096 + at_across + (tp ^ f) * 32, 512);
                         else
-                            p[h][i] = lds16(lp + tp * 2048 + (at0 ^ (h * 64)));
+                            p[h][i] = lds16(lp + tp * 2048 + (at0 ^ (h * 64)) +
+                                            (4 * h + g + p_behind[i] < 8 ? 0 : later));
                         if constexpr (kQAcross)
                             q[h][i] = lds_across(lq + h * 4096 + at_across + (tq ^ f) * 32, 512);
                         else
-                            q[h][i] = lds16(lq + tq * 2048 + (at0 ^ (h * 64)));
+                            q[h][i] = lds16(lq + tq * 2048 + (at0 ^ (h * 64)) +
+                                            (4 * h + g + q_behind[i] < 8 ? 0 : later));
                     }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -236,7 +287,7 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16(p[h][i], q[h][j], acc[i][j]);
-                stage = (stage + 1) % kSmallStages;
+                stage = next;
             }
             meet<0, 0>();   // the copies behind the last block are in, its reads done
         }
@@ -875,8 +926,17 @@ int launch_small(Bf16Args& a, hipStream_t stream) {
         a.tiles = max_tiles(a.M, a.G, kSmall) * a.tiles_w;
     }
     clear_hip_error();
-    hipLaunchKernelGGL(bf16_small_kernel<MODE>, dim3(loop_grid(a.tiles, kSmallThreads)),
-                       dim3(kSmallThreads), 0, stream, a);
+    a.places = MODE == kRowsBack || MODE == kWeightBack ? ceil_div(a.tiles, 8 * kRun) * 8 * kRun : a.tiles;
+    const dim3 grid(loop_grid(a.places, kSmallThreads));
+    const uint64_t lines = (uintptr_t)a.p | (uintptr_t)a.q | (uint64_t)a.pitch_p * 2 | (uint64_t)a.pitch_q * 2;
+    if constexpr (MODE == kForward || MODE == kGate) {
+        if (lines % 128 != 0) {
+            hipLaunchKernelGGL((bf16_small_kernel<MODE, false>), grid, dim3(kSmallThreads), 0, stream, a);
+            EP_HIP_CHECK(hipGetLastError());
+            return EP_OK;
+        }
+    }
+    hipLaunchKernelGGL((bf16_small_kernel<MODE, true>), grid, dim3(kSmallThreads), 0, stream, a);
     EP_HIP_CHECK(hipGetLastError());
     return EP_OK;
 }
@@ -906,23 +966,25 @@ int launch_big(Bf16Args& a, hipStream_t stream) {
 
 // Which tiles take less time, from what each kind costs (ns):
 //   small  the weights once from memory (5.4 TB/s) or once for every 64 rows from cache
-//          (7.5 TB/s), a third more where their rows do not begin on lines; 4 us
+//          (7.5 TB/s), for the rows' gradient a third more where the weights' rows do not
+//          begin on lines; 4 us
 //   big    rounds of tiles over the CUs, 1.25 us a block of c; 10 us, for the gate 20; no
 //          less than the weights at 4.4 TB/s
 // Small : big, us, as measured (rows an expert; e: even, s: falling off as 1 / rank):
 //   forward, 8 experts of 7168 x 1792   1  39 : 47   32 e  43 : 46   64 e 50 : 46   256 e 118 : 55
 //   forward, 8 of 3584 x 7168          64 e  91 : 139  128 e 144 : 143  192 s 198 : 146
-//   forward, 24 of 1808 x 2184         16 e  53 : 63    64 s  76 : 72   256 e 169 : 78
+//   forward, 24 of 1808 x 2184         16 e  41 : 62    64 s  62 : 72   256 e 139 : 78
 //   forward, 1 of 7168 x 1792         512  29 : 44    32 of 512 x 1024  128 e 18 : 27  512 s 50 : 32
 //   rows, 8 of 7168 x 1792             64 e  49 : 133  256 e 138 : 156  512 s 247 : 156
 //   rows, 8 of 3584 x 7168              1  83 : 79   128 e 155 : 86
+//   rows, 8 of 7168 x 1800              1  44 : 141  256 e 166 : 142   64 e of 24 of 1808 x 2184 63 : 47
 template <int MODE>
 bool big_takes_less(const Bf16Args& a) {
     const double experts = a.G < a.M ? a.G : (double)a.M;     // that can have rows
     const double weights = 2.0 * a.W * a.C;
     const double per64 = (double)(a.M / kSmall) + 0.5 * experts;
     double small = fmax(experts * weights / 5400.0, per64 * weights / 7500.0);
-    if (a.pitch_p % kDepth != 0) small *= 4.0 / 3.0;
+    if (MODE == kRowsBack && a.pitch_p % kDepth != 0) small *= 4.0 / 3.0;
     const double row_tiles = fmax(experts, (double)(a.M / kBig) + 0.5 * experts);
     const double columns = MODE == kGate ? ceil_div(a.W / 2, kBig / 2) : ceil_div(a.W, kBig);
     const double rounds = ceil(row_tiles * columns / kBigGrid);

@@ -103,6 +103,33 @@ def test_product_backward(ep, sizes, N, K, first, behind, whole, kind):
     assert torch.equal(r, grad_rows) and torch.equal(w, grad_w) and int(c.st) == 0
 
 
+@pytest.mark.parametrize("rows_at,w_at", [(0, 1), (3, 0), (7, 7), (1, 4), (5, 2)])
+@pytest.mark.parametrize("K", [8, 56, 64, 72, 256, 328, 520])
+def test_operands_off_lines(ep, rows_at, w_at, K):
+    """Tensors that begin 16 bytes times rows_at and w_at behind a line, NaN around them."""
+    log(f"[bf16 product off lines] rows {rows_at} w {w_at} K={K}")
+    c = Case([3, 0, 66, 17], 80, K, whole=True, seed=13)
+
+    def moved(x, at):
+        room = torch.full((x.numel() + 192,), float("nan"), **BF)
+        room = room[-room.data_ptr() % 128 // 2:]
+        y = room[8 * at:][:x.numel()].view(x.shape)
+        assert y.data_ptr() % 128 == 16 * at
+        return y.copy_(x)
+
+    rows, w, grad_out = moved(c.rows, rows_at), moved(c.w, w_at), moved(c.grad_out, w_at)
+    out, grad_rows = torch.full((c.M, c.N), POISON, **BF), torch.full((c.M, K), POISON, **BF)
+    grad_w, h, pre = torch.full_like(w, POISON), torch.full((c.M, 40), POISON, **BF), torch.full((c.M, 80), POISON, **BF)
+    ep.ep_expert_product_bf16(rows, c.off, w, out, c.st)
+    ep.ep_expert_product_bf16_backward(rows, c.off, w, grad_out, grad_rows, grad_w, c.st, c.workspace(ep))
+    ep.ep_expert_gate_up_bf16(rows, c.off, w, pre, h, c.st)
+    assert int(c.st) == 0
+    c.check(out, *X.product64(c.rows, c.off, c.w), K, "out")
+    c.check(grad_rows, *X.product64(c.grad_out, c.off, c.w.transpose(1, 2)), c.N, "grad_rows")
+    c.close(grad_w, *X.weights64(c.rows, c.off, c.grad_out), 66, "grad_w")
+    c.check(pre, *X.product64(c.rows, c.off, c.w), K, "pre")
+
+
 GATES = [([1], 8, 8, 0, 0), ([3], 24, 72, 2, 1), ([64], 32, 64, 0, 0), ([65], 40, 136, 0, 3), ([0, 5, 0, 0, 70, 1], 200, 264, 7, 9),
          ([1] * 8, 520, 328, 0, 0), ([31, 128, 2, 63], 136, 1000, 0, 5), ([0, 0], 64, 128, 4, 4), ([17] * 70, 40, 48, 1, 1),
          ([300, 256], 256, 512, 0, 0), ([700, 0, 33], 264, 520, 3, 0)]
