@@ -342,7 +342,7 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
 // much again from LDS and took 5 % longer.
 //
 // Bound by the card's power: with random numbers in the operands a block takes 1.38 us
-// (clock lowered to about 1.6 GHz), with zeros 1.06; a bare loop of these MFMAs (16 x 16 x
+// (clock lowered to about 1.7 GHz), with zeros 1.06; a bare loop of these MFMAs (16 x 16 x
 // 32; 32 x 32 x 16 draw more) reaches 2.0 PFLOP/s with random numbers.  8192 x 8192 x
 // 7168, the card warm: forward 1.46 PFLOP/s, rows' gradient 1.33, weights' 1.33; the
 // library's product of the same operands 1.6, 1.2, 0.9.  About 8 us a tile go to its
