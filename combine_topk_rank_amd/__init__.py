@@ -689,9 +689,10 @@ def _bf16_args(rows, group_offset, w, device, weights=None, width=None):
     if sized.dim() != 3:
         raise ValueError("w must be [G, N, K]")
     G, N, K = sized.shape
-    if rows is None and width is None:
-        _need("rows", rows)
-    M = rows.shape[0] if rows is not None else width.shape[0]
+    counted = rows if rows is not None else _need("rows", width)
+    if counted.dim() != 2:
+        raise ValueError("rows and grad_out must be [M, K] and [M, N]")
+    M = counted.shape[0]
     return (G, M, N, K, _arg("rows", rows, _BF16, (M, K), device),
             _arg("group_offset", _need("group_offset", group_offset), _I32, (G + 1,), device),
             _arg("w", w, _BF16, (G, N, K), device))
@@ -1199,10 +1200,10 @@ class BuffersMoETrain(BuffersLL):
         if self._saved is None:
             raise RuntimeError("backward() needs a forward() before it")
         weight, w_gate_up, w_down, mode, token_mask, logits = self._saved
-        self._saved = None
         s, off = self.shape, self.expert_offset
         ep_combine_ll_backward(s, self.y, self.topk_idx, self.topk_w, self.expert_slot, grad_out,
                                self.y, self.grad_topk_w, self.dev_status)
+        self._saved = None      # not before: a refused grad_out leaves the forward as it was
         ep_expert_product_bf16_backward(self.inner, off, w_down, self.y, self.grad_inner,
                                         self.grad_down, self.dev_status, self.back_workspace)
         ep_expert_gate_up_bf16_backward(self.rows, off, w_gate_up, self.pre, self.grad_inner,

@@ -448,3 +448,15 @@ def test_refusals(ep):
     odd = Case([4], 12, 72)
     with pytest.raises(ep.EpError):
         ep.ep_expert_product_bf16(odd.rows, odd.off, odd.w, torch.zeros(4, 12, **BF), odd.st)
+
+
+def test_rows_without_two_dimensions(ep):
+    c = Case([4, 5], 64, 72)
+    out, gw = torch.zeros(9, 64, **BF), torch.zeros(2, 64, 72, **BF)
+    for rows in (c.rows[0], c.rows[0, 0], c.rows[None]):
+        with pytest.raises(ValueError):
+            ep.ep_expert_product_bf16(rows, c.off, c.w, out, c.st)
+        with pytest.raises(ValueError):
+            ep.ep_expert_product_bf16_backward(rows, c.off, None, c.grad_out, None, gw, c.st)
+    with pytest.raises(ValueError):
+        ep.ep_expert_product_bf16_backward(None, c.off, c.w, c.grad_out[0, 0], torch.zeros(9, 72, **BF), None, c.st)

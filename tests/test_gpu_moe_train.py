@@ -133,6 +133,19 @@ def test_backward_needs_its_forward(ep):
         ep.BuffersMoETrain(ep.shape(T, 128, E, 2, k, ep.EP_FMT_FP8_E4M3_B128), F)
 
 
+def test_a_refused_backward_leaves_the_forward(ep):
+    T, H, E, F, k = 20, 64, 8, 32, 2
+    d = make(T, H, E, F, 2)
+    buf = ep.BuffersMoETrain(ep.shape(T, H, E, 2, k), F)
+    run = lambda: buf.forward(d["x"], None, d["weight"], EPS, lambda n: n.float() @ d["router"].t(), d["w1"], d["w2"])  # noqa: E731
+    run()
+    first = buf.backward(d["grad_out"]).clone()
+    run()
+    with pytest.raises(ValueError):
+        buf.backward(d["grad_out"][:-1])
+    assert torch.equal(buf.backward(d["grad_out"]), first)
+
+
 def test_captured(ep):
     """A whole step in a graph, replayed on other inputs with eager work between."""
     T, H, E, F, k = 300, 128, 16, 64, 4
