@@ -1175,6 +1175,7 @@ class BuffersMoETrain(BuffersLL):
         """router(normed) gives the logits [T, E] (bf16 or float32).  Returns the combined
         output; self.residual is the residual stream that it belongs to, self.balance_loss the
         balance loss."""
+        self._saved = None      # one that ends early leaves no forward to go back from
         ep_rmsnorm(x, residual, weight, eps, None if residual is None else self.residual,
                    self.normed, None, self.rstd)
         if residual is None:

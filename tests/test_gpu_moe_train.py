@@ -218,3 +218,27 @@ def test_the_rank_layout_between_the_products(ep):
     gx, gw = torch.autograd.grad(out, (x64, w64), d["grad_out"].double())
     near(grad_x, gx, "grad_x", 2.0 ** -7)
     near(grad_w, gw, "grad_w", 1e-5)
+
+
+def test_a_forward_that_ends_early_leaves_no_forward(ep):
+    """Its buffers hold parts of two steps then: no backward may take them for one."""
+    T, H, E, F, k = 20, 64, 8, 32, 2
+    d = make(T, H, E, F, 2)
+    buf = ep.BuffersMoETrain(ep.shape(T, H, E, 2, k), F)
+    router = lambda n: n.float() @ d["router"].t()  # noqa: E731
+    run = lambda x=d["x"], r=router, w2=d["w2"]: buf.forward(x, None, d["weight"], EPS, r, d["w1"], w2)  # noqa: E731
+    run()
+    first = buf.backward(d["grad_out"]).clone()
+
+    def no_router(n):
+        raise KeyError("router")
+
+    for kind, bad in ((KeyError, dict(r=no_router)), (ValueError, dict(w2=d["w2"].float())), (ValueError, dict(x=d["x"].float())),
+                      (ValueError, dict(r=lambda n: router(n)[:, :4]))):
+        run()
+        with pytest.raises(kind):
+            run(**bad)
+        with pytest.raises(RuntimeError, match="forward"):
+            buf.backward(d["grad_out"])
+    run()
+    assert torch.equal(buf.backward(d["grad_out"]), first)
