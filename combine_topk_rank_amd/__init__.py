@@ -1195,16 +1195,22 @@ class BuffersMoETrain(BuffersLL):
     def backward(self, grad_out, grad_residual=None, grad_balance_loss=None, router_backward=None):
         """grad_out bf16 [T, H]; grad_residual that of self.residual, grad_balance_loss (float32
         [1], on the device) that of self.balance_loss, or None.  router_backward(grad_logits)
-        gives the gradient of router's input, bf16 [T, H], or None.  Returns the gradient of x (and
-        of residual); the weights' are self.grad_weight, self.grad_gate_up and self.grad_down."""
+        gives the gradient of router's input, bf16 [T, H], or None; if it raises, or gives another
+        tensor, the forward is used up.  Returns the gradient of x (and of residual); the weights'
+        are self.grad_weight, self.grad_gate_up and self.grad_down."""
         import torch
         if self._saved is None:
             raise RuntimeError("backward() needs a forward() before it")
         weight, w_gate_up, w_down, mode, token_mask, logits = self._saved
         s, off = self.shape, self.expert_offset
+        # Every gradient that is given, before the first launch: y and pre become their own
+        # gradients, and a call that is refused later would have used the forward up.
+        device, _ = _call_device(None)
+        _arg("grad_residual", grad_residual, _BF16, (s.T, s.H), device)
+        _arg("grad_balance_loss", grad_balance_loss, _F32, (1,), device)
         ep_combine_ll_backward(s, self.y, self.topk_idx, self.topk_w, self.expert_slot, grad_out,
                                self.y, self.grad_topk_w, self.dev_status)
-        self._saved = None      # not before: a refused grad_out leaves the forward as it was
+        self._saved = None      # not before: a refused gradient leaves the forward as it was
         ep_expert_product_bf16_backward(self.inner, off, w_down, self.y, self.grad_inner,
                                         self.grad_down, self.dev_status, self.back_workspace)
         ep_expert_gate_up_bf16_backward(self.rows, off, w_gate_up, self.pre, self.grad_inner,

@@ -242,3 +242,27 @@ def test_a_forward_that_ends_early_leaves_no_forward(ep):
             buf.backward(d["grad_out"])
     run()
     assert torch.equal(buf.backward(d["grad_out"]), first)
+
+
+def test_a_backward_refused_for_any_gradient_leaves_the_forward(ep):
+    T, H, E, F, k = 20, 64, 8, 32, 2
+    d = make(T, H, E, F, 2)
+    buf = ep.BuffersMoETrain(ep.shape(T, H, E, 2, k), F)
+    run = lambda: buf.forward(d["x"], None, d["weight"], EPS, lambda n: n.float() @ d["router"].t(), d["w1"], d["w2"])  # noqa: E731
+    good = dict(grad_out=d["grad_out"], grad_residual=d["grad_residual"], grad_balance_loss=d["grad_loss"])
+    run()
+    first = buf.backward(**good).clone()
+    run()
+    for name, t in good.items():
+        for bad in (t.double(), t[:0], t.cpu(), torch.cat([t, t])):
+            with pytest.raises(ValueError, match=name):
+                buf.backward(**{**good, name: bad})
+    with pytest.raises(ValueError, match="grad_residual"):
+        buf.backward(**{**good, "grad_residual": torch.zeros(H, T, dtype=torch.bfloat16, device="cuda").t()})
+    assert torch.equal(buf.backward(**good), first)
+    # the router's part comes when the forward's values have become their gradients
+    run()
+    with pytest.raises(ValueError, match="grad_other"):
+        buf.backward(**good, router_backward=lambda g: g)
+    with pytest.raises(RuntimeError, match="forward"):
+        buf.backward(**good)
