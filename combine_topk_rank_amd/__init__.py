@@ -1096,7 +1096,7 @@ class BuffersMoE(BuffersLL):
         if residual is None:    # the call has no residual sum to store then
             import torch
             with torch.cuda.stream(stream):
-                self.residual.copy_(x)
+                self.residual.copy_(x.detach())    # no part of x's graph
 
     def route(self, logits, mode=EP_GATE_SOFTMAX_RENORM, token_mask=None, stream=None):
         ep_route(logits, token_mask, mode, self.topk_idx, self.topk_w, stream=stream)
@@ -1179,7 +1179,7 @@ class BuffersMoETrain(BuffersLL):
         ep_rmsnorm(x, residual, weight, eps, None if residual is None else self.residual,
                    self.normed, None, self.rstd)
         if residual is None:
-            self.residual.copy_(x)
+            self.residual.copy_(x.detach())    # no part of x's graph
         logits = router(self.normed)
         ep_route(logits, token_mask, mode, self.topk_idx, self.topk_w, self.num_choices,
                  self.num_tokens, self.lse, self.balance_loss, self.route_workspace)

@@ -228,3 +228,17 @@ def test_block_of_padded_tokens_alone(ep):
     assert int(buf.dev_status) == 0 and int(buf.expert_offset.abs().max()) == 0
     assert (out == 0).all()
     assert torch.equal(buf.residual, R.norm64(d["x"], d["residual"], d["weight"], EPS)[0])
+
+
+def test_an_input_of_autograd(ep):
+    """x may be a tensor that autograd follows: the buffers take no part in it."""
+    T, H, E, k, F = 20, 256, 8, 2, 128
+    d = make(T, H, E, F, 9)
+    buf = ep.BuffersMoE(ep.shape(T, H, E, 2, k, ep.EP_FMT_FP8_E4M3_B128), F)
+    x = d["x"].clone().requires_grad_(True)
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        buf.norm(x, None, d["weight"], EPS, stream=stream)
+        assert not buf.residual.requires_grad and buf.residual.grad_fn is None
+        torch.cuda.synchronize()
+        assert torch.equal(buf.residual, d["x"])

@@ -266,3 +266,18 @@ def test_a_backward_refused_for_any_gradient_leaves_the_forward(ep):
         buf.backward(**good, router_backward=lambda g: g)
     with pytest.raises(RuntimeError, match="forward"):
         buf.backward(**good)
+
+
+def test_an_input_of_autograd(ep):
+    """x may be a tensor that autograd follows, as an embedding's: the buffers take no part in it."""
+    T, H, E, F, k = 20, 64, 8, 32, 2
+    d = make(T, H, E, F, 2)
+    buf = ep.BuffersMoETrain(ep.shape(T, H, E, 2, k), F)
+    table = d["x"].clone().requires_grad_(True)
+    for residual in (None, d["residual"]):
+        for _ in range(2):
+            x = table * 1.0
+            out = buf.forward(x, residual, d["weight"], EPS, lambda n: n.float() @ d["router"].t(), d["w1"], d["w2"])
+            assert not any(t.requires_grad for t in (out, buf.residual, buf.normed)) and buf.residual.grad_fn is None
+            x.backward(buf.backward(d["grad_out"]))
+        assert torch.isfinite(table.grad).all()
