@@ -1126,6 +1126,7 @@ class BuffersMoETrain(BuffersLL):
     """Buffers of a mixture-of-experts block's training pass over per-expert rows in bf16
     (``s.fmt`` EP_FMT_BF16): norm, router with its balance loss, dispatch, the experts' two
     products of inner width ``F`` and combine, and their gradients in the opposite order.
+    ``weights_dtype``: that of the experts' weights' gradients, bfloat16 or float32.
 
     ``forward`` and ``backward`` run on the current stream.  A backward belongs to the forward
     before it and uses up what that left (self.y and self.pre get their gradients)."""
@@ -1135,6 +1136,8 @@ class BuffersMoETrain(BuffersLL):
         import torch
         if s.fmt != EP_FMT_BF16:
             raise ValueError("the experts take bf16 rows: fmt must be EP_FMT_BF16")
+        if weights_dtype not in (None, torch.bfloat16, torch.float32):
+            raise ValueError(f"weights_dtype must be float32 or bfloat16, is {weights_dtype}")
         super().__init__(s, capacity_rows, device)
         T, H, E, k, cap = s.T, s.H, s.E, s.k, self.capacity_rows
         bf = dict(dtype=torch.bfloat16, device=device)

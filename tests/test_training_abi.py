@@ -199,3 +199,10 @@ def test_clip_refuses(ep):
     # nothing to launch
     assert clip(ep, listed(ep, at=None)) == 0
     assert clip(ep, listed(ep, 0, 0, at=None)) == 0
+
+
+def test_a_block_with_weights_gradients_of_no_such_type(ep):
+    import torch
+    for kind in (torch.float16, torch.float64, torch.int32):
+        with pytest.raises(ValueError, match="weights_dtype"):
+            ep.BuffersMoETrain(ep.shape(4, 64, 8, 4, 2), 32, weights_dtype=kind, device="cpu")
