@@ -78,6 +78,12 @@ EP_FUSED_ONE_KERNEL_LARGE = 102
 EP_FUSED_TWO_CALLS = 103
 EP_FMT_BF16 = 0
 EP_FMT_FP8_E4M3_B128 = 1
+EP_PRODUCT_FORWARD = 0
+EP_PRODUCT_GATE_UP = 1
+EP_PRODUCT_ROWS_BACKWARD = 2
+EP_PRODUCT_WEIGHTS_BACKWARD = 3
+EP_TILES_SMALL = 111
+EP_TILES_BIG = 112
 EP_BF16 = 0
 EP_F32 = 1
 EP_GATE_SOFTMAX = 0
@@ -187,6 +193,8 @@ def _load() -> ctypes.CDLL:
     L.ep_expert_product_bf16.restype = ctypes.c_int
     L.ep_expert_gate_up_bf16.argtypes = [i32, i64, i32, i32, P, P, P, P, P, P, P]
     L.ep_expert_gate_up_bf16.restype = ctypes.c_int
+    L.ep_expert_bf16_plan.argtypes = [i32, i32, i64, i32, i32]
+    L.ep_expert_bf16_plan.restype = ctypes.c_int
     L.ep_expert_backward_workspace_bytes.argtypes = [i32, i64, i32, i32]
     L.ep_expert_backward_workspace_bytes.restype = sz
     L.ep_expert_product_bf16_backward.argtypes = [i32, i64, i32, i32, i32, P, P, P, P, P, P, P, P,
@@ -717,6 +725,15 @@ def ep_expert_gate_up_bf16(rows, group_offset, w, pre, out, dev_status, stream=N
                                     _arg("out", _need("out", out), _BF16, (M, N // 2), device),
                                     _status(dev_status, device), st_)
     _check(st, "ep_expert_gate_up_bf16")
+
+
+def ep_expert_bf16_plan(product: int, G: int, M: int, N: int, K: int) -> int:
+    """EP_TILES_SMALL or EP_TILES_BIG: the tiles that one of the EP_PRODUCT_* products of rows
+    [M, K] and weights [G, N, K] takes."""
+    st = lib.ep_expert_bf16_plan(product, G, M, N, K)
+    if st not in (EP_TILES_SMALL, EP_TILES_BIG):
+        _check(st, "ep_expert_bf16_plan")
+    return st
 
 
 def ep_expert_backward_workspace_bytes(G: int, M: int, N: int, K: int) -> int:

@@ -993,8 +993,8 @@ bool big_takes_less(const Bf16Args& a) {
 }
 
 template <int MODE>
-int launch(Bf16Args& a, hipStream_t stream) {
-    return big_takes_less<MODE>(a) ? launch_big<MODE, false>(a, stream) : launch_small<MODE>(a, stream);
+bool takes_big(const Bf16Args& a) {
+    return big_takes_less<MODE>(a);
 }
 
 // The weights' gradient: big tiles write it faster (8 rows of 8 experts, 7168 x 1792:
@@ -1003,12 +1003,32 @@ int launch(Bf16Args& a, hipStream_t stream) {
 // 512 x 1024, 256 rows each, falling off as 1 / rank 37 : 50 us, even 36 : 20; 512 each 51 :
 // 87 and 50 : 26).
 template <>
-int launch<kWeightBack>(Bf16Args& a, hipStream_t stream) {
+bool takes_big<kWeightBack>(const Bf16Args& a) {
     const int64_t tiles = (int64_t)a.G * a.splits * ceil_div(a.V, kBig) * ceil_div(a.W, kBig);
-    if (a.G > 1 && a.splits == 1 && tiles < 2 * kBigGrid && a.M >= 32 * kBig)
-        return launch_small<kWeightBack>(a, stream);
-    return a.wide ? launch_big<kWeightBack, true>(a, stream)
-                  : launch_big<kWeightBack, false>(a, stream);
+    return a.G == 1 || a.splits > 1 || tiles >= 2 * kBigGrid || a.M < 32 * kBig;
+}
+
+template <int MODE>
+int launch(Bf16Args& a, hipStream_t stream) {
+    if (!takes_big<MODE>(a)) return launch_small<MODE>(a, stream);
+    if constexpr (MODE == kWeightBack)
+        if (a.wide) return launch_big<MODE, true>(a, stream);
+    return launch_big<MODE, false>(a, stream);
+}
+
+// What the rules look at, of the products from rows [M, K] and weights [G, N, K].
+void forward_sizes(Bf16Args& a, int32_t N, int32_t K) {
+    a.W = N;
+    a.C = a.pitch_p = a.pitch_q = K;
+}
+void rows_back_sizes(Bf16Args& a, int32_t N, int32_t K) {
+    a.W = a.pitch_p = K;
+    a.C = a.pitch_q = N;
+}
+void weight_back_sizes(Bf16Args& a, int32_t N, int32_t K) {
+    a.W = a.pitch_p = K;
+    a.V = a.pitch_q = N;
+    a.splits = weight_splits(a.G, a.M, N, K);
 }
 
 int forward(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
@@ -1027,8 +1047,7 @@ int forward(int32_t G, int64_t M, int32_t N, int32_t K, const void* rows,
     a.q = reinterpret_cast<const uint16_t*>(rows);
     a.out = out;
     a.pre = reinterpret_cast<uint16_t*>(pre);
-    a.W = N;
-    a.C = a.pitch_p = a.pitch_q = K;
+    forward_sizes(a, N, K);
     return gate ? launch<kGate>(a, stream) : launch<kForward>(a, stream);
 }
 
@@ -1047,20 +1066,16 @@ int backward(Bf16Args a, int32_t N, int32_t K, int32_t dtype, const void* rows, 
              const void* grad_out, void* grad_rows, void* grad_w, void* workspace,
              hipStream_t stream) {
     a.q = reinterpret_cast<const uint16_t*>(grad_out);
-    a.pitch_p = K;
-    a.pitch_q = N;
-    a.W = K;
     if (grad_rows && a.M > 0) {
+        rows_back_sizes(a, N, K);
         a.p = reinterpret_cast<const uint16_t*>(w);
         a.out = grad_rows;
-        a.C = N;
         const int v = launch<kRowsBack>(a, stream);
         if (v != EP_OK) return v;
     }
     if (!grad_w) return EP_OK;
+    weight_back_sizes(a, N, K);
     a.p = reinterpret_cast<const uint16_t*>(rows);
-    a.V = N;
-    a.splits = weight_splits(a.G, a.M, N, K);
     a.wide = dtype == EP_F32 || a.splits > 1;
     a.out = a.splits > 1 ? workspace : grad_w;
     const int v = launch<kWeightBack>(a, stream);
@@ -1099,6 +1114,36 @@ extern "C" int ep_expert_gate_up_bf16(int32_t G, int64_t M, int32_t F, int32_t K
                                       void* out, int32_t* dev_status, hipStream_t stream) {
     if (F < 8 || F % 8 != 0 || F > kMaxDim / 2) return EP_ERR_INVALID_ARG;
     return forward(G, M, 2 * F, K, rows, group_offset, w, pre, out, dev_status, true, stream);
+}
+
+extern "C" int ep_expert_bf16_plan(int32_t product, int32_t G, int64_t M, int32_t N, int32_t K) {
+    if (check_bf16(G, M, N, K) != EP_OK || (product == EP_PRODUCT_GATE_UP && N % 16 != 0))
+        return EP_ERR_INVALID_ARG;
+    Bf16Args a{};
+    a.G = G;
+    a.M = M;
+    a.splits = 1;
+    bool big = false;
+    switch (product) {
+        case EP_PRODUCT_FORWARD:
+            forward_sizes(a, N, K);
+            big = takes_big<kForward>(a);
+            break;
+        case EP_PRODUCT_GATE_UP:
+            forward_sizes(a, N, K);
+            big = takes_big<kGate>(a);
+            break;
+        case EP_PRODUCT_ROWS_BACKWARD:
+            rows_back_sizes(a, N, K);
+            big = takes_big<kRowsBack>(a);
+            break;
+        case EP_PRODUCT_WEIGHTS_BACKWARD:
+            weight_back_sizes(a, N, K);
+            big = takes_big<kWeightBack>(a);
+            break;
+        default: return EP_ERR_INVALID_ARG;
+    }
+    return big ? EP_TILES_BIG : EP_TILES_SMALL;
 }
 
 extern "C" size_t ep_expert_backward_workspace_bytes(int32_t G, int64_t M, int32_t N, int32_t K) {

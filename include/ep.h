@@ -589,6 +589,22 @@ int ep_expert_gate_up_bf16_backward(int32_t G, int64_t M, int32_t F, int32_t K, 
                                     void* grad_rows, void* grad_w, int32_t* dev_status,
                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Which tiles a product takes for these sizes (rows [M,K], weights [G,N,K]; N = 2F for the
+ * gate's product): EP_TILES_SMALL (64 x 64 results) or EP_TILES_BIG (256 x 256);
+ * EP_ERR_INVALID_ARG for sizes that its call refuses.  The results are right with
+ * either.  Host only, launches nothing. */
+enum ep_product {
+    EP_PRODUCT_FORWARD = 0,            /* ep_expert_product_bf16 */
+    EP_PRODUCT_GATE_UP = 1,            /* ep_expert_gate_up_bf16 */
+    EP_PRODUCT_ROWS_BACKWARD = 2,      /* grad_rows of either backward call */
+    EP_PRODUCT_WEIGHTS_BACKWARD = 3    /* grad_w of either backward call */
+};
+enum {   /* distinct from every status code */
+    EP_TILES_SMALL = 111,
+    EP_TILES_BIG = 112
+};
+int ep_expert_bf16_plan(int32_t product, int32_t G, int64_t M, int32_t N, int32_t K);
+
 /* A tensor of a list: n elements of dtype EP_BF16 or EP_F32 at data (device
  * memory, aligned to the element; NULL with n = 0).  n < 2^38. */
 typedef struct ep_tensor {

@@ -206,3 +206,22 @@ def test_a_block_with_weights_gradients_of_no_such_type(ep):
     for kind in (torch.float16, torch.float64, torch.int32):
         with pytest.raises(ValueError, match="weights_dtype"):
             ep.BuffersMoETrain(ep.shape(4, 64, 8, 4, 2), 32, weights_dtype=kind, device="cpu")
+
+
+def test_which_tiles(ep):
+    """The plan of the bf16 products: one row an expert is a weight stream through small tiles, a training batch's rows go
+    through big ones; what the calls refuse is refused."""
+    plan, small, big = ep.ep_expert_bf16_plan, ep.EP_TILES_SMALL, ep.EP_TILES_BIG
+    for p in (ep.EP_PRODUCT_FORWARD, ep.EP_PRODUCT_GATE_UP, ep.EP_PRODUCT_ROWS_BACKWARD):
+        assert plan(p, 8, 8, 7168, 1792) == small and plan(p, 8, 8192, 7168, 1792) == big
+    p = ep.EP_PRODUCT_WEIGHTS_BACKWARD
+    assert plan(p, 8, 8, 7168, 1792) == big and plan(p, 32, 8192, 512, 1024) == small
+    assert plan(p, 1, 100_000, 64, 64) == big           # in parts
+    L = ep.lib.ep_expert_bf16_plan
+    for bad in ((-1, 2, 9, 64, 72), (4, 2, 9, 64, 72), (0, 0, 9, 64, 72), (0, 4097, 9, 64, 72), (0, 2, -1, 64, 72), (0, 2, 1 << 31, 64, 72),
+                (0, 2, 9, 12, 72), (0, 2, 9, 64, 76), (0, 2, 9, (1 << 20) + 8, 72), (1, 2, 9, 72, 72)):
+        assert L(*bad) == INVALID, bad
+        with pytest.raises(ep.EpError):
+            plan(*bad)
+    assert all(L(p, G, M, N, K) in (small, big) for p in range(4) for G in (1, 70, 4096) for M in (0, 1, 10 ** 6, 2 ** 31 - 1)
+               for N in (16, 4096, 1 << 20) for K in (8, 4096, 1 << 20))
