@@ -1,0 +1,107 @@
+"""The bf16 expert products as they are called: their own forward differenced."""
+
+import pytest
+import torch
+
+import training_refs as X
+from test_gpu_expert_bf16 import BF, POISON, Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ep():
+    import combine_topk_rank_amd as ep
+    return ep
+
+
+def tiles(ep, c):
+    return "".join("B" if ep.ep_expert_bf16_plan(p, c.G, c.M, c.N, c.K) == ep.EP_TILES_BIG else "s" for p in range(4) if p != 1)
+
+
+def ones(c, *shape):
+    return torch.randint(-1, 2, shape, device="cuda", generator=c.gen).bfloat16()
+
+
+@pytest.mark.parametrize("sizes,N,K,takes", [([40, 0, 25], 72, 120, "ssB"), ([20000], 2064, 120, "BsB"), ([20000], 120, 2064, "sBB")])
+def test_differences_of_the_products_own_forward(ep, sizes, N, K, takes):
+    """Central differences of ep_expert_product_bf16 against its gradients, in a direction for
+    the rows and one for the weights.
+
+    All operands are -1, 0 or 1, so rows and weights with the step added or taken away are
+    -2 to 2.  With K <= 120 every output is a whole number up to 240 and exact in bf16; so is the
+    rows' gradient with N <= 120.  The longer products have 64 values other than 0 in a row (and,
+    for the rows' gradient, in a column), so that the same holds.  The weights' gradient is taken
+    in float.  Each side is a whole number below 2^53: the two are equal."""
+    c = Case(sizes, N, K, whole=True, seed=31)
+    assert tiles(ep, c) == takes
+    M, G = c.M, c.G
+    c.rows, c.w, c.grad_out = ones(c, M, K), ones(c, G, N, K), ones(c, M, N)
+    step_r, step_w = ones(c, M, K), ones(c, G, N, K)
+    if K > 120:
+        for t in (c.rows, step_r):
+            t[:, 64:] = 0
+    if N > 120:
+        c.grad_out[:, 64:] = 0
+    gr, gw = torch.zeros(M, K, **BF), torch.zeros(G, N, K, device="cuda")
+    ep.ep_expert_product_bf16_backward(c.rows, c.off, c.w, c.grad_out, gr, gw, c.st, c.workspace(ep))
+
+    def f(rows, w):
+        out = torch.zeros(M, N, **BF)
+        ep.ep_expert_product_bf16(rows, c.off, w, out, c.st)
+        assert float(out.abs().max()) <= 256
+        return out.double()
+
+    assert float(gr.abs().max()) <= 256
+    d = c.grad_out.double()
+    by_rows = (d * (f(c.rows + step_r, c.w) - f(c.rows - step_r, c.w))).sum() / 2
+    by_w = (d * (f(c.rows, c.w + step_w) - f(c.rows, c.w - step_w))).sum() / 2
+    assert by_rows == (gr.double() * step_r.double()).sum() != 0
+    assert by_w == (gw.double() * step_w.double()).sum() != 0
+    assert int(c.st) == 0
+
+
+def test_differences_of_the_gates_own_forward(ep):
+    """Central differences of ep_expert_gate_up_bf16 against the weights' gradient that its
+    backward makes.
+
+    A row of rows is one at its own c, so out[m, f] = silu(w[f, m]) * w[F + f, m] and each weight
+    reaches one output.  Gates -1 to 4, ups 1/2 to 2 and the step h = 1/4 are exact in bf16.
+    Each output is rounded once (2^-8) after a few float operations (8 * 2^-24 * 4); the weights'
+    gradient is that of a grad_pre rounded once.  Along an up the output is linear; along a
+    gate the quotient is off by h^2 / 6 * max |silu'''| * up, and |silu'''| = |3 s'' + g s'''| <=
+    3 * 0.0963 + 4.25 * 0.125 = 0.83 (s'' and s''' the sigmoid's, at gates up to 4.25)."""
+    F, K, h = 72, 64, 0.25
+    g = torch.Generator(device="cuda").manual_seed(32)
+    eighths = lambda lo, hi, *s: torch.randint(lo, hi + 1, s, device="cuda", generator=g) / 8  # noqa: E731
+    w = torch.cat([eighths(-8, 32, 1, F, K), eighths(4, 16, 1, F, K)], 1).bfloat16()
+    rows = torch.eye(K, **BF)
+    d = (0.5 + eighths(0, 8, K, F)).bfloat16()
+    off, st = torch.tensor([0, K], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def f(w):
+        out = torch.zeros(K, F, **BF)
+        ep.ep_expert_gate_up_bf16(rows, off, w, None, out, st)
+        return out.double()
+
+    pre, out = torch.zeros(K, 2 * F, **BF), torch.zeros(K, F, **BF)
+    ep.ep_expert_gate_up_bf16(rows, off, w, pre, out, st)
+    assert torch.equal(pre, w[0].t())
+    gp, gw = torch.zeros(K, 2 * F, **BF), torch.zeros(1, 2 * F, K, device="cuda")
+    ep.ep_expert_gate_up_bf16_backward(rows, off, w, pre, d, gp, None, gw, st,
+                                       torch.empty(max(16, ep.ep_expert_backward_workspace_bytes(1, K, 2 * F, K)), dtype=torch.uint8, device="cuda"))
+    assert torch.equal(gw[0], gp.t().float())
+    once = X.U_BF16 + 32 * X.U32
+    for part in (slice(0, F), slice(F, 2 * F)):
+        step = torch.zeros_like(w)
+        step[:, part] = h
+        up, down = f(w + step), f(w - step)
+        quotient = d.double() * (up - down) / (2 * h)
+        off_by = d.double() * once * (up.abs() + down.abs()) / (2 * h) * (1 + once)
+        if part.start == 0:
+            off_by = off_by + d.double() * h * h / 6 * 0.83 * w[0, F:].t().double()
+        got = gw[0, part].t().double()
+        assert ((got - quotient).abs() <= off_by + got.abs() * once).all()
+        # all together: much nearer than a factor or the other half would be
+        assert float((got - quotient).sum().abs() / quotient.sum()) <= 0.02
+    assert int(st) == 0
