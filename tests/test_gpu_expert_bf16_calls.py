@@ -1,4 +1,6 @@
-"""The bf16 expert products as they are called: their own forward differenced."""
+"""The bf16 expert products as they are called: their own forward differenced, and calls
+whose weights' gradient is summed in parts through a workspace, on two streams and in a
+graph, with big and with small tiles."""
 
 import pytest
 import torch
@@ -105,3 +107,76 @@ def test_differences_of_the_gates_own_forward(ep):
         # all together: much nearer than a factor or the other half would be
         assert float((got - quotient).sum().abs() / quotient.sum()) <= 0.02
     assert int(st) == 0
+
+
+SPLIT = [([5000, 0, 9000], 264, 520, "ssB"), ([9000, 5000], 1040, 520, "BBB")]
+
+
+@pytest.mark.parametrize("sizes,N,K,takes", SPLIT)
+def test_two_streams_with_sums_in_parts(ep, sizes, N, K, takes):
+    """Two backward calls at once, on streams of their own, each with its own workspace."""
+    cases = [Case(s, N, K, whole=True, seed=33 + i) for i, s in enumerate((sizes, sizes[::-1]))]
+    outs = [(torch.full((c.M, K), POISON, **BF), torch.full((c.G, N, K), POISON, device="cuda"), c.workspace(ep)) for c in cases]
+    assert all(tiles(ep, c) == takes and ws is not None for c, (_, _, ws) in zip(cases, outs))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for c, (gr, gw, ws), s in zip(cases, outs, (None, side)):
+            ep.ep_expert_product_bf16_backward(c.rows, c.off, c.w, c.grad_out, gr, gw, c.st, ws, s)
+    torch.cuda.synchronize()
+    for c, (gr, gw, _) in zip(cases, outs):
+        c.check(gr, *X.product64(c.grad_out, c.off, c.w.transpose(1, 2)), N, "grad_rows")
+        c.close(gw, *X.weights64(c.rows, c.off, c.grad_out), max(sizes), "grad_w")
+        assert int(c.st) == 0
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes,N,K,takes", [([5000, 0, 9000], 528, 136, "ssB"), ([9000, 0, 5000], 2064, 520, "BBB")])
+def test_captured_with_sums_in_parts(ep, sizes, N, K, takes, kind):
+    """Gate, product and both backward calls in one graph, replayed on other inputs and offsets
+    with the program's own work between."""
+    c = Case(sizes, N, K, seed=34)
+    F, M = N // 2, c.M
+    down = Case(sizes, K, F, seed=35)          # the second product, from the gate's outputs
+    assert tiles(ep, c) == takes
+    ws, ws2 = c.workspace(ep), down.workspace(ep)
+    assert ws is not None and ws2 is not None
+    c.w *= K ** -0.5
+    down.w *= F ** -0.5
+    pre, inner, out = torch.zeros(M, N, **BF), torch.zeros(M, F, **BF), torch.zeros(M, K, **BF)
+    gi, gp, gr = torch.zeros(M, F, **BF), torch.zeros(M, N, **BF), torch.zeros(M, K, **BF)
+    gw, gw2 = torch.zeros(c.G, N, K, dtype=kind, device="cuda"), torch.zeros(c.G, K, F, dtype=kind, device="cuda")
+
+    def step():
+        ep.ep_expert_gate_up_bf16(c.rows, c.off, c.w, pre, inner, c.st)
+        ep.ep_expert_product_bf16(inner, c.off, down.w, out, c.st)
+        ep.ep_expert_product_bf16_backward(inner, c.off, down.w, down.grad_out, gi, gw2, c.st, ws2)
+        ep.ep_expert_gate_up_bf16_backward(c.rows, c.off, c.w, pre, gi, gp, gr, gw, c.st, ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    a, b = sizes[0], M
+    for i, off in enumerate(([0, a, a, b], [0, 1, b - 1, b], [0, 0, 0, b], [10, 300, a, b - 20])):
+        c.off.copy_(torch.tensor(off, dtype=torch.int32))
+        c.rows.copy_(c.values(M, K))
+        outs = (pre, inner, out, gi, gp, gr, gw, gw2)
+        for t in outs:
+            t.fill_(POISON)
+        step()
+        want = [t.clone() for t in outs]
+        for t in outs:
+            t.fill_(POISON)
+        ws.fill_(0xFF)
+        ws2.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want)), i
+        assert all(torch.isfinite(t.float()).all() for t in outs)
+    assert int(c.st) == 0
