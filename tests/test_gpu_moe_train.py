@@ -281,3 +281,52 @@ def test_an_input_of_autograd(ep):
             assert not any(t.requires_grad for t in (out, buf.residual, buf.normed)) and buf.residual.grad_fn is None
             x.backward(buf.backward(d["grad_out"]))
         assert torch.isfinite(table.grad).all()
+
+
+# no token; one; a mask that leaves none
+@pytest.mark.parametrize("T,masked", [(0, False), (1, True), (40, True)])
+def test_a_block_without_rows(ep, T, masked):
+    """No expert has a row: no output, no gradient but what goes past the block."""
+    H, E, F, k = 64, 8, 32, 2
+    d = make(T, H, E, F, 6)
+    mask = torch.zeros(T, dtype=torch.uint8, device="cuda") if masked else None
+    for kind in (torch.bfloat16, torch.float32):
+        buf = ep.BuffersMoETrain(ep.shape(T, H, E, 2, k), F, weights_dtype=kind)
+        for t in (buf.grad_gate_up, buf.grad_down, buf.grad_weight, buf.out, buf.y, buf.pre):
+            t.fill_(float("nan"))
+        out = buf.forward(d["x"], d["residual"], d["weight"], EPS, lambda n: n.float() @ d["router"].t(), d["w1"], d["w2"], token_mask=mask)
+        assert out.shape == (T, H) and (out == 0).all() and float(buf.balance_loss) == 0.0
+        grad_x = buf.backward(d["grad_out"], d["grad_residual"], d["grad_loss"], lambda g: (g @ d["router"]).bfloat16())
+        assert int(buf.dev_status) == 0
+        assert torch.equal(grad_x, d["grad_residual"])
+        for t in (buf.grad_gate_up, buf.grad_down, buf.grad_weight):
+            assert (t == 0).all()
+        s, n = torch.ones(1, dtype=torch.float64, device="cuda"), torch.ones(1, device="cuda")
+        ep.ep_grad_norm(buf.gradients(), s, n, torch.zeros(ep.ep_grad_norm_workspace_bytes(), dtype=torch.uint8, device="cuda"))
+        assert float(n) == 0.0
+
+
+@pytest.mark.parametrize("T,H,E,k,F,takes", [(1024, 264, 256, 8, 72, "ss"), (4096, 1024, 256, 8, 520, "BB")])
+def test_a_block_of_256_experts(ep, T, H, E, k, F, takes):
+    """More experts than a wavefront has lanes, about T k / E rows each, through small and big tiles."""
+    d = make(T, H, E, F, 7)
+    buf = ep.BuffersMoETrain(ep.shape(T, H, E, 32, k), F)
+    plans = [ep.ep_expert_bf16_plan(p, E, T * k, 2 * F, H) for p in (ep.EP_PRODUCT_GATE_UP, ep.EP_PRODUCT_ROWS_BACKWARD)]
+    assert "".join("B" if p == ep.EP_TILES_BIG else "s" for p in plans) == takes
+    seen = {}
+
+    def router(n):
+        seen["n"] = n
+        return n.float() @ d["router"].t()
+
+    out = buf.forward(d["x"], d["residual"], d["weight"], EPS, router, d["w1"], d["w2"])
+    got_out, got_loss = out.clone(), buf.balance_loss.clone()
+    grad_x = buf.backward(d["grad_out"], d["grad_residual"], d["grad_loss"], lambda g: (g @ d["router"]).bfloat16())
+    assert int(buf.dev_status) == 0
+    want, loss, grads = reference(d, buf.topk_idx, None, 1, k)
+    near(got_out, want, "out")
+    near(got_loss, loss.view(1), "loss")
+    near(grad_x, grads["x"], "grad_x")
+    near(buf.grad_weight, grads["weight"], "grad_weight")
+    near(buf.grad_gate_up, grads["w1"], "grad_gate_up")
+    near(buf.grad_down, grads["w2"], "grad_down")
