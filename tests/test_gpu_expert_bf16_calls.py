@@ -180,3 +180,50 @@ def test_captured_with_sums_in_parts(ep, sizes, N, K, takes, kind):
         assert all(torch.equal(x, y) for x, y in zip(outs, want)), i
         assert all(torch.isfinite(t.float()).all() for t in outs)
     assert int(c.st) == 0
+
+
+@pytest.mark.parametrize("rows,takes", [(70, "ssB"), (6000, "BBB")])
+def test_far_weights(ep, rows, takes):
+    """Weights whose bytes lie beyond 2^32: 40 experts of 8192 x 8192, 5.4 GB, rows at two of them."""
+    G, N, K = 40, 8192, 8192
+    g = torch.Generator(device="cuda").manual_seed(36)
+    whole = lambda *s: torch.randint(-2, 3, s, device="cuda", generator=g).bfloat16()  # noqa: E731
+    w = torch.zeros(G, N, K, **BF)
+    w[0], w[G - 1] = whole(N, K), whole(N, K)
+    M = 3 + rows
+    off = torch.tensor([0] + [3] * (G - 1) + [M], dtype=torch.int32, device="cuda")
+    x, d, st = whole(M, K), whole(M, N), torch.zeros(1, dtype=torch.int32, device="cuda")
+    plan = [ep.ep_expert_bf16_plan(p, G, M, N, K) for p in (ep.EP_PRODUCT_FORWARD, ep.EP_PRODUCT_ROWS_BACKWARD, ep.EP_PRODUCT_WEIGHTS_BACKWARD)]
+    assert "".join("B" if p == ep.EP_TILES_BIG else "s" for p in plan) == takes
+    out, gr, gw = torch.full((M, N), POISON, **BF), torch.full((M, K), POISON, **BF), torch.full((G, N, K), POISON, **BF)
+    ep.ep_expert_product_bf16(x, off, w, out, st)
+    n = ep.ep_expert_backward_workspace_bytes(G, M, N, K)
+    ep.ep_expert_product_bf16_backward(x, off, w, d, gr, gw, st, torch.empty(n, dtype=torch.uint8, device="cuda") if n else None)
+    assert int(st) == 0
+    for e, a, b in ((0, 0, 3), (G - 1, 3, M)):      # every sum below 2^24: exact in float
+        assert torch.equal(out[a:b].double(), (x[a:b].double() @ w[e].double().t().contiguous()).bfloat16().double())
+        assert torch.equal(gr[a:b].double(), (d[a:b].double() @ w[e].double()).bfloat16().double())
+        assert torch.equal(gw[e].double(), (d[a:b].double().t().contiguous() @ x[a:b].double()).bfloat16().double())
+    assert (gw[1:G - 1] == 0).all()
+
+
+@pytest.mark.parametrize("rows,N", [(300, 72), (9000, 2056)])
+def test_far_rows(ep, rows, N):
+    """Rows whose bytes lie beyond 2^32: the last ones of 300 000 x 8192, 4.9 GB."""
+    M, K = 300_000, 8192
+    g = torch.Generator(device="cuda").manual_seed(37)
+    whole = lambda *s: torch.randint(-2, 3, s, device="cuda", generator=g).bfloat16()  # noqa: E731
+    x, d, w = torch.zeros(M, K, **BF), torch.zeros(M, N, **BF), whole(2, N, K)
+    a = M - rows
+    x[a:], d[a:] = whole(rows, K), whole(rows, N)
+    off, st = torch.tensor([a, a + 100, M], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, gr, gw = torch.full((M, N), POISON, **BF), torch.full((M, K), POISON, **BF), torch.full((2, N, K), POISON, device="cuda")
+    ep.ep_expert_product_bf16(x, off, w, out, st)
+    n = ep.ep_expert_backward_workspace_bytes(2, M, N, K)
+    ep.ep_expert_product_bf16_backward(x, off, w, d, gr, gw, st, torch.empty(n, dtype=torch.uint8, device="cuda") if n else None)
+    assert int(st) == 0
+    assert (out[:a] == POISON).all() and (gr[:a] == POISON).all()
+    for e, lo, hi in ((0, a, a + 100), (1, a + 100, M)):
+        assert torch.equal(out[lo:hi].double(), (x[lo:hi].double() @ w[e].double().t().contiguous()).bfloat16().double())
+        assert torch.equal(gr[lo:hi].double(), (d[lo:hi].double() @ w[e].double()).bfloat16().double())
+        assert torch.equal(gw[e].double(), d[lo:hi].double().t().contiguous() @ x[lo:hi].double())

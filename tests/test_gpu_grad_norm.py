@@ -252,3 +252,20 @@ def test_refusals(ep):
     ep.ep_grad_norm([], s, n, ws)
     assert float(s) == 0.0 and float(n) == 0.0
     ep.ep_grad_clip([], s, 1.0)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_a_tensor_of_more_than_2_to_the_31_elements(ep, kind):
+    n = 2 ** 31 + 20_011
+    at = [0, 1, 2 ** 30, 2 ** 31 - 1, 2 ** 31, n - 16385, n - 1]
+    flat = torch.zeros(n + 5, dtype=kind, device="cuda")
+    flat[n:] = 7.0                      # behind it
+    t = flat[:n]
+    for i, j in enumerate(at):
+        t[j] = float(i + 1)
+    s, norm = run(ep, [t, torch.full((3,), 2.0, device="cuda")])
+    assert float(s) == sum((i + 1) ** 2 for i in range(len(at))) + 12
+    root = math.sqrt(float(s))
+    ep.ep_grad_clip([t], s, root / 2)
+    assert [float(t[j]) for j in at] == [(i + 1) / 2 for i in range(len(at))]
+    assert (flat[n:] == 7.0).all() and int((t != 0).sum()) == len(at)
