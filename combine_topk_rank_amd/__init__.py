@@ -44,6 +44,7 @@ The functions keep the C names:
     ep_expert_gate_up_bf16(rows, group_offset, w, pre, out, dev_status, stream=None)
     ep_expert_gate_up_bf16_backward(rows, group_offset, w, pre, grad_out, grad_pre, grad_rows,
                                     grad_w, dev_status, workspace=None, stream=None)
+    ep_expert_bf16_plan(product, G, M, N, K)   # the tiles that one of the EP_PRODUCT_* takes
     ep_grad_norm(tensors, sum_squares, norm, workspace, stream=None)
     ep_grad_clip(tensors, sum_squares, max_norm, into=None, stream=None)
         (these take their sizes from the tensors, or check them against the shape: a wrong

@@ -347,8 +347,8 @@ __global__ __launch_bounds__(kSmallThreads, 2) void bf16_small_kernel(Bf16Args a
 // 7168, the card warm: forward 1.46 PFLOP/s, rows' gradient 1.33, weights' 1.33; the
 // library's product of the same operands 1.6, 1.2, 0.9.  About 8 us a tile go to its
 // beginning and end, 4 of them to stores, which all CUs have at once: 7680 rows of 8
-// experts, 7168 x 1792, 183 us (1.08 PFLOP/s; 34 row tiles for 30 tiles' rows, and 3.7
-// rounds of the CUs run as four).
+// experts, 7168 x 1792, 184 to 192 us (1.03 to 1.07 PFLOP/s; 34 row tiles for 30 tiles' rows,
+// and 3.7 rounds of the CUs run as four).
 constexpr int kBig = 256;
 constexpr int kBigThreads = 256;
 constexpr int kBigCopies = 8;                   // a wavefront's copies of a block of an operand
@@ -978,6 +978,8 @@ int launch_big(Bf16Args& a, hipStream_t stream) {
 //   rows, 8 of 7168 x 1792             64 e  49 : 133  256 e 138 : 156  512 s 247 : 156
 //   rows, 8 of 3584 x 7168              1  83 : 79   128 e 155 : 86
 //   rows, 8 of 7168 x 1800              1  44 : 141  256 e 166 : 142   64 e of 24 of 1808 x 2184 63 : 47
+// (The bound by the weights is too high for the rows' gradient of 3584 x 7168: 98 us for the
+// 79 that big tiles take with one row an expert.  The small ones it takes there are 5 % slower.)
 template <int MODE>
 bool big_takes_less(const Bf16Args& a) {
     const double experts = a.G < a.M ? a.G : (double)a.M;     // that can have rows

@@ -14,8 +14,9 @@
 // range still scales what float holds.
 //
 // Bound by memory.  40 tensors of 622 MB, nearly all bf16: norm 111 us (5.6 TB/s), clip
-// into other buffers 241 us (5.2), both in a row 330: the clip finds the last 200 MB in the
-// last-level cache.  1000 tensors of 156 MB: norm 33 us.
+// into other buffers 241 us (5.2), both in a row 337: the clip finds the last 200 MB in the
+// last-level cache.  1000 tensors of 156 MB: norm 37 us.  The same bytes all in float: norm
+// 113 and 40 us, clip of the 622 MB 260 us; all in bf16 126, 42 and 233.
 
 #include <string.h>
 
